@@ -248,15 +248,6 @@ int moe_combine_grad(const moe_plan *p, const void *dY, const void *Ys, const in
 
 namespace mswz {
 
-int64_t w4_workspace_bytes(const W4Args &) { return 0; }
-
-hipError_t launch_w4(const W4Args &a, hipStream_t stream)
-{
-    if (a.bf16)
-        return a.e2m1 ? launch_w4_bf16_e2m1(a, stream) : launch_w4_bf16_u4(a, stream);
-    return a.e2m1 ? launch_w4_f16_e2m1(a, stream) : launch_w4_f16_u4(a, stream);
-}
-
 hipError_t launch_grouped(const GroupedArgs &a, hipStream_t stream)
 {
     if (a.k_axis)

@@ -4,21 +4,31 @@
 //
 // The weights are streamed once from memory straight into registers, turned
 // into 16-bit MFMA operands there (exactly: 4-bit values have few significant
-// bits) and multiplied against the activations with 16x16x32 MFMAs; a scale
-// multiplies the fp32 sum of its group, so no weight is rounded.
+// bits) and multiplied against the activations with 16x16x32 MFMAs, for one
+// row as for sixteen: the MFMA takes 16 cycles per 512 weights, less than the
+// conversions, which a dot product on the vector unit would come on top of.
+// A scale multiplies the fp32 sum of its group, so no weight is rounded.
 //
-// One workgroup of eight waves owns 16*NB columns of D and 16*MB rows; its
-// waves split K in chunks of 128 (64 bytes of every weight row per wave and
-// load, 512 bytes of a row by the workgroup's eight neighbours), each keeps
-// fp32 sums of its own, and the sums meet in LDS at the end, added in wave
-// order.
+// One workgroup of eight waves owns up to ROWS rows and 16*NB*NG columns of D.
+// Its waves split the columns NG ways and K KQ ways (NG * KQ = 8): a step is
+// 128*KQ values of K, of which each wave takes 128 (64 bytes of each of its
+// weight rows).  Few rows need no sharing of A and take KQ = 8, so that a
+// workgroup requests 512 consecutive bytes of each weight row; 64 rows take
+// KQ = 2, so that A, which every workgroup reads from L2, serves more columns.
+// Weights are loaded into registers, A and the scales into an LDS stage by
+// direct copies, kAhead steps early; a step's barrier waits for its own copies
+// and leaves the later steps' loads in flight.  (Scales and zero points loaded
+// by the lanes that use them, two or three bytes each from sixteen rows, took
+// longer than the weights: one row by 16384 x 8192 in 33 us, 18 us without.)
 //
 // Lane l = (r, q) = (l % 16, l / 16) loads 16 bytes of weight row r, K block q
-// (32 values) of the chunk.  MFMA j multiplies dword j of every lane.  The K
-// order inside the chunk is free as long as A follows it, but a scale group
-// must not be shared by one MFMA with another one: for groups shorter than the
-// chunk the lanes' dwords are exchanged first (two or four lane swaps per 16
-// bytes) so that each MFMA's 32 K values lie in one group.
+// (32 values) of the wave's 128.  MFMA j multiplies dword j of every lane.  The
+// K order inside the 128 is free as long as A follows it, but a scale group
+// must not be shared by one MFMA with another one: for shorter groups the
+// lanes' dwords are exchanged first (two or four lane swaps per 16 bytes) so
+// that each MFMA's 32 K values lie in one group.  FP4 weights with bf16
+// activations skip that: the conversion itself multiplies by the block's
+// power of two, exactly.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -32,64 +42,50 @@
 namespace mswz {
 namespace {
 
-constexpr int kW4Waves = 8;
-constexpr int kChunk = 128;     // K values of one 16-byte load of all four lane groups
+constexpr int kW4Threads = 512;
+constexpr int kChunk = 128;               // K values of one 16-byte load of all four lane groups
+constexpr int kStages = 4, kAhead = 3;    // LDS stages of A and register slots; steps in flight
 
-typedef uint32_t u32v2 __attribute__((ext_vector_type(2)));
-
-// Four 4-bit integers at bits 0-3, 4-7, 8-11, 12-15 of both halves of a dword
-// become four pairs of 16-bit floats: pair i holds the values at bits 4i and
-// 16 + 4i, i.e. elements i and i + 4 of the dword's eight.
-//   fp16: 1024 + q has q in the last bits of its significand; subtracting
-//         1024 + z is exact, and so is q - z;
-//   bf16: 1 + q/16 has q in the upper four of its seven significand bits; the
-//         product sum is corrected by (1 + z/16) times the sum of A and
-//         multiplied by 16 s.
+// Eight 4-bit integers of a dword as 16-bit floats, in element order.  A byte
+// 0..15 read as E4M3 is that many times 2^-9 (subnormal up to 7, the first
+// normal binade from 8), so the conversion with the factor 2^9 gives the
+// integer; both 16-bit formats hold it exactly, and fp16 its difference to the
+// zero point z (twice in zz) as well.
 template <bool BF16>
 __device__ __forceinline__ u32x4 u4_values(uint32_t w, uint32_t zz)
 {
-    u32x4 v;
+    const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+    const uint32_t lo = __builtin_amdgcn_perm(odd, even, 0x05010400u), hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);
     if constexpr (BF16) {
-        v[0] = ((w << 3) & 0x00780078u) | 0x3f803f80u;
-        v[1] = ((w >> 1) & 0x00780078u) | 0x3f803f80u;
-        v[2] = ((w >> 5) & 0x00780078u) | 0x3f803f80u;
-        v[3] = ((w >> 9) & 0x00780078u) | 0x3f803f80u;
+        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true))};
     } else {
         typedef _Float16 h2 __attribute__((ext_vector_type(2)));
         const h2 z = __builtin_bit_cast(h2, zz);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t b = ((w >> (4 * i)) & 0x000f000fu) | 0x64006400u;
-            v[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, b) - z);
-        }
+        auto sub = [&](auto v) { return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, v) - z); };
+        return u32x4{sub(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, false)),
+                     sub(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, true)),
+                     sub(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, false)),
+                     sub(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, true))};
     }
-    return v;
 }
 
-// Eight E2M1 values, in element order.
+// Eight E2M1 values times a power of two, in element order.
 template <bool BF16>
-__device__ __forceinline__ u32x4 e2m1_values(uint32_t w)
+__device__ __forceinline__ u32x4 e2m1_values(uint32_t w, float scale)
 {
-    u32x4 v;
-    if constexpr (BF16) {
-        v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0));
-        v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1));
-        v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2));
-        v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3));
-    } else {
-        v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0));
-        v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1));
-        v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2));
-        v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3));
-    }
-    return v;
-}
-
-// A's eight values in the order u4_values gives the weights: (0,4)(1,5)(2,6)(3,7).
-__device__ __forceinline__ u32x4 u4_order(u32x4 a)
-{
-    return u32x4{__builtin_amdgcn_perm(a[2], a[0], 0x05040100u), __builtin_amdgcn_perm(a[2], a[0], 0x07060302u),
-                 __builtin_amdgcn_perm(a[3], a[1], 0x05040100u), __builtin_amdgcn_perm(a[3], a[1], 0x07060302u)};
+    if constexpr (BF16)
+        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3))};
+    else
+        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 0)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 1)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 2)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 3))};
 }
 
 __device__ __forceinline__ void swap32(uint32_t &a, uint32_t &b)
@@ -106,8 +102,8 @@ __device__ __forceinline__ void swap16(uint32_t &a, uint32_t &b)
 }
 
 // SPAN: K values that share a scale inside a chunk, 32, 64 or 128.  After
-// w4_arrange dword j of lane group q holds K block kb, dword kw of the chunk,
-// so that MFMA j's values lie in one span.
+// w4_arrange dword j of lane group q holds eight-value piece w4_piece of the
+// chunk, so that MFMA j's values lie in one span.
 template <int SPAN>
 __device__ __forceinline__ void w4_arrange(u32x4 &w)
 {
@@ -123,14 +119,28 @@ __device__ __forceinline__ void w4_arrange(u32x4 &w)
     }
 }
 template <int SPAN>
-__device__ __forceinline__ int w4_koff(int j, int q)
+__device__ __forceinline__ int w4_piece(int j, int q)
 {
     if constexpr (SPAN == 128)
-        return 32 * q + 8 * j;
+        return 4 * q + j;
     else if constexpr (SPAN == 64)
-        return 32 * ((q & 1) + 2 * (j >> 1)) + 8 * ((j & 1) + 2 * (q >> 1));
+        return 4 * ((q & 1) + 2 * (j >> 1)) + (j & 1) + 2 * (q >> 1);
     else
-        return 32 * j + 8 * q;
+        return 4 * j + q;
+}
+
+// A's stage holds a row's pieces next to each other (a copy instruction then
+// reads 512 bytes or more of one row: rows of a power-of-two pitch lie in the
+// same L2 channel, and 64 bytes of each of 16 rows took twice as long), piece c
+// of row m at place c ^ row_key(m).  A 16-byte LDS read serves the lanes
+// together that agree in lane bits 1 and 5: eight rows that share bit 1, and
+// two lane groups' pieces, whose numbers differ in bit 2 (bit 0 for 32-value
+// spans).  The key takes the other three bits from the eight rows, so that the
+// sixteen reads fall into different banks.
+template <int SPAN>
+__host__ __device__ constexpr int row_key(int m)
+{
+    return SPAN == 32 ? (m & 1) << 1 | (m & 2) >> 1 | (m & 12) : (m & 1) | (m & 4) >> 1 | (m & 2) << 1 | (m & 8);
 }
 
 // 2^(e - 127), e = 255 NaN
@@ -155,33 +165,120 @@ struct W4Kernel {
     const uint8_t *Z;
     const int32_t *offsets;
     void *D;
+    float *ws;            // SPLIT: fp32 partials [part][M][N]
     int M, N, K, E;
-    int group, groups;
+    uint64_t group_magic; // floor(c * group_magic / 2^32) = c / (chunks that share a scale)
+    int groups;
     int lda, ldd;
     int beta;
+    int part_steps;       // steps of one part of K
 };
 
-template <bool BF16, bool E2M1, int SPAN, int MB, int NB, int OUT>
-__global__ void __launch_bounds__(64 * kW4Waves)
+template <bool BF16, bool E2M1, int SPAN, int ROWS, int NB, int NG, int OUT, bool SPLIT>
+__global__ void __launch_bounds__(kW4Threads)
 w4_kernel(W4Kernel p)
 {
-    constexpr int kTiles = MB * NB;
-    __shared__ __attribute__((aligned(16))) float red[kW4Waves][kTiles][64][4];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 15, q = lane >> 4;
-    const int n0 = blockIdx.x * (16 * NB);
-    int e = 0, tile = blockIdx.y, lo = 0, hi = p.M;
-    if (p.offsets && !group_of_tile(p.offsets, p.E, p.M, 16 * MB, blockIdx.y, lane, e, tile, lo, hi))
-        return;
-    const int m0 = lo + 16 * MB * tile, rows = min(hi - m0, 16 * MB);
+    constexpr int KQ = 8 / NG, MB = ROWS < 16 ? 1 : ROWS / 16;
+    constexpr bool kPre = E2M1 && BF16;             // scales folded into the conversion
+    constexpr bool kSums = BF16 && !E2M1;           // zero points applied to sums of A
+    static_assert(!kPre || SPAN == 128, "folded scales need no lane swaps");
+    constexpr int kSpans = 128 / SPAN, kPer = 4 / kSpans;   // scale groups of a chunk, MFMAs of one
+    constexpr int kCols = 16 * NB * NG;
+    // A's part of a stage, in whole copies by all waves (what lies behind the
+    // rows is written as zeros and not read)
+    constexpr int kCopies = (ROWS * KQ * 16 + kW4Threads - 1) / kW4Threads, kABytes = kCopies * kW4Threads * 16;
+    static_assert(4 * NB * MB * 1024 <= kABytes, "the waves' sums fit into two stages");
+    // A step's scales of one column lie next to each other in memory, at any
+    // byte; they are copied as the aligned words that hold them.  Scales are
+    // copied by waves 0-3 and zero points by 4-7 (FP4: scales by all).
+    constexpr int kSize = E2M1 ? 1 : 2;                       // bytes of a scale
+    constexpr int kPerCol = KQ * (kPre ? 4 : kSpans);         // scales of a column and step
+    constexpr int kSWords = (kPerCol * kSize + 4 - kSize + 3) / 4, kZWords = E2M1 ? 0 : (kPerCol + 3 + 3) / 4;
+    constexpr int kSThreads = E2M1 ? kW4Threads : kW4Threads / 2;
+    constexpr int kSCopies = (kCols * kSWords + kSThreads - 1) / kSThreads;
+    constexpr int kSBytes = kSCopies * kSThreads * 4;         // (whole copies: what lies behind is not read)
+    constexpr int kStageBytes = kABytes + (E2M1 ? 1 : 2) * kSBytes;
+    // one named array per stage: the compiler then knows which stage a copy
+    // writes, and waits for no other one
+    __shared__ __attribute__((aligned(1024))) uint8_t st0[kStageBytes], st1[kStageBytes], st2[kStageBytes], st3[kStageBytes];
+    auto stage = [&](int u) { return u == 0 ? st0 : u == 1 ? st1 : u == 2 ? st2 : st3; };
 
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, q = lane >> 4, ng = wave % NG, kq = wave / NG;
+    const int n0 = blockIdx.x * kCols;
+    int e = 0, tile = blockIdx.y, lo = 0, hi = p.M;
+    if (p.offsets && !group_of_tile(p.offsets, p.E, p.M, ROWS, blockIdx.y, lane, e, tile, lo, hi))
+        return;
+    const int m0 = lo + ROWS * tile, rows = min(hi - m0, ROWS);
+    const int all_steps = (p.K + kChunk * KQ - 1) / (kChunk * KQ);
+    const int first = SPLIT ? int(blockIdx.z) * p.part_steps : 0;
+    const int steps = SPLIT ? min(p.part_steps, all_steps - first) : all_steps;
+
+    // ---- per-lane offsets of the loads.  Rows beyond N or the tile, and K values
+    // beyond K, point at the ends of the buffers' ranges and read as zeros; by
+    // selects, since with a branch for the last step a register might be the
+    // target of either side's load and every load in flight was waited for.
     const uint32_t row_bytes = uint32_t(p.K) / 2;
     const uint32_t w_bytes = uint32_t(p.N) * row_bytes;
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.B + size_t(e) * w_bytes, w_bytes);
     const uint32_t a_bytes = uint32_t(rows - 1) * uint32_t(p.lda) * 2 + uint32_t(p.K) * 2;
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.A + size_t(m0) * p.lda * 2, a_bytes);
-    // scales of this lane's weight rows (rows beyond N repeat the last one)
-    const size_t sbase = size_t(e) * p.N * p.groups;
+    const uint32_t count = uint32_t(p.N) * uint32_t(p.groups);
+    // aligned start of this matrix's scales (or zero points), the bytes to their
+    // first one, and the range in whole words
+    const bool zeros = !E2M1 && wave >= 4;
+    const uint64_t s_start = reinterpret_cast<uint64_t>(p.S) + uint64_t(e) * count * kSize;
+    const uint64_t z_start = reinterpret_cast<uint64_t>(p.Z) + uint64_t(e) * count;
+    const uint32_t s_skip = uint32_t(s_start) & 3, z_skip = uint32_t(z_start) & 3;
+    const uint32_t s_bytes = zeros ? (p.Z ? (z_skip + count + 3) & ~3u : 0) : (s_skip + count * kSize + 3) & ~3u;
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(reinterpret_cast<const void *>((zeros ? z_start : s_start) & ~uint64_t(3)), s_bytes);
+    uint32_t w_off[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int n = n0 + 16 * (NB * ng + nb) + r;
+        w_off[nb] = n < p.N ? uint32_t(n) * row_bytes + uint32_t(64 * kq + 16 * q) : w_bytes;
+    }
+    // word copies: word u % words of column u / words
+    uint32_t s_off[kSCopies], s_word[kSCopies];
+#pragma unroll
+    for (int i = 0; i < kSCopies; ++i) {
+        const uint32_t u = uint32_t(tid % kSThreads + kSThreads * i), words = zeros ? kZWords : kSWords;
+        const uint32_t col = u / words, n = n0 + col;
+        s_word[i] = 4 * (u - col * words);
+        s_off[i] = col < kCols && n < uint32_t(p.N) ? (zeros ? z_skip : s_skip) + n * uint32_t(p.groups) * (zeros ? 1 : kSize) : ~0u;
+    }
+    auto group_of = [&](int c) {   // first scale of chunk c
+        return kPre ? 4 * c : SPAN < 128 ? kSpans * c : int((uint64_t(c) * p.group_magic) >> 32);
+    };
+    uint32_t a_off[kCopies];
+    int a_k[kCopies];
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+        // unit u of the stage: [row][piece's place]
+        const int u = tid + kW4Threads * i, m = u / (16 * KQ);
+        a_k[i] = 8 * (u % (16 * KQ) ^ row_key<SPAN>(m));
+        a_off[i] = m < rows ? uint32_t(m * p.lda + a_k[i]) * 2 : a_bytes;
+    }
+
+    u32x4 w[kStages][NB];
+    // all loads of step t (a step beyond the last repeats it: never used)
+    auto load = [&](int slot, uint8_t *st, int t) {
+        const int c0 = (first + min(t, steps - 1)) * KQ;          // first chunk of the step
+        const uint32_t kb = uint32_t(c0) * 64;
+        const int left = p.K - c0 * kChunk;     // K values from the step's first on
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i)
+            buffer_load_lds16(ra, st + 16 * (kW4Threads * i + 64 * wave), a_k[i] < left ? a_off[i] + kb * 4 : a_bytes, 0);
+        const uint32_t g0 = uint32_t(group_of(c0)) * (zeros ? 1 : kSize);
+#pragma unroll
+        for (int i = 0; i < kSCopies; ++i)
+            buffer_load_lds4(rs, st + kABytes + (zeros ? kSBytes : 0) + 4 * (kSThreads * i + 64 * (wave % (kSThreads / 64))),
+                             s_off[i] == ~0u ? s_bytes : ((s_off[i] + g0) & ~3u) + s_word[i], 0);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+            w[slot][nb] = buffer_load16(rw, kChunk * kq + 32 * q < left ? w_off[nb] + kb : w_bytes, 0);
+    };
+    constexpr int kLoads = kCopies + kSCopies + NB;   // vector-memory operations of one step
 
     f32x4 acc[NB][MB];
 #pragma unroll
@@ -189,107 +286,172 @@ w4_kernel(W4Kernel p)
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
             acc[nb][mb] = f32x4{};
-    const uint32_t one = BF16 ? 0x3f803f80u : 0x3c003c00u;
-    const u32x4 ones = {one, one, one, one};
+    const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 
-    const int chunks = (p.K + kChunk - 1) / kChunk;
-    for (int c = wave; c < chunks; c += kW4Waves) {
-        const int k0 = c * kChunk;
-        u32x4 w[NB];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const uint32_t row = n0 + 16 * nb + r;
-            const uint32_t off = row * row_bytes + uint32_t(k0 / 2 + 16 * q);
-            w[nb] = buffer_load16(rw, int(row) < p.N && k0 + 32 * q < p.K ? off : w_bytes, 0);
-            w4_arrange<SPAN>(w[nb]);
-        }
-        u32x4 a[MB][4];
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = k0 + w4_koff<SPAN>(j, q), m = 16 * mb + r;
-                const u32x4 v = buffer_load16(ra, m < rows && k < p.K ? uint32_t(m * p.lda + k) * 2 : a_bytes, 0);
-                a[mb][j] = E2M1 ? v : u4_order(v);
-            }
-        // the chunk's spans: MFMAs 4 s / spans ..
-        constexpr int kSpans = 128 / SPAN, kPer = 4 / kSpans;
-#pragma unroll
-        for (int s = 0; s < kSpans; ++s) {
-            if (k0 + SPAN * s >= p.K)
-                break;
-            const int g = (k0 + SPAN * s) / p.group;
-            f32x4 asum[MB];
-            if constexpr (BF16 && !E2M1) {
-#pragma unroll
-                for (int mb = 0; mb < MB; ++mb) {
-                    asum[mb] = f32x4{};
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j)
-                        asum[mb] = mfma_16x16x32<BF16>(a[mb][kPer * s + j], ones, asum[mb]);
-                }
-            }
+    // A's fragments: piece c of row r of block mb
+    auto piece = [&](const uint8_t *st, int mb, int j) {
+        const int m = (16 * mb + r) % ROWS;
+        return lds_read16(st, 16 * uint32_t((m * KQ + kq) * 16 + (w4_piece<SPAN>(j, q) ^ row_key<SPAN>(m))));
+    };
+    // scale (zero point) g of the chunk for this lane's column of block nb; t is
+    // the step that the stage holds.  A whole chunk without scales (behind K)
+    // has no value of A either, but a scale that is not finite would still count.
+    auto scale_of = [&](const uint8_t *st, int t, int nb, int g, bool z) {
+        const int c0 = (first + t) * KQ, gi = group_of(c0 + kq) + g, col = 16 * (NB * ng + nb) + r;
+        const uint32_t size = z ? 1 : kSize, skip = z ? z_skip : s_skip;
+        const uint32_t at = skip + (uint32_t(n0 + col) * uint32_t(p.groups) + uint32_t(group_of(c0))) * size;
+        const uint8_t *b = st + kABytes + (z ? kSBytes : 0) + 4 * (z ? kZWords : kSWords) * col + (at & 3) +
+                           (gi - group_of(c0)) * size;
+        const uint32_t v = size == 2 ? *reinterpret_cast<const uint16_t *>(b) : *b;
+        return gi < p.groups ? v : 0u;
+    };
+    auto compute = [&](const uint8_t *st, int slot, int t) {
+        if constexpr (kPre) {
+            float scale[NB];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-                const size_t si = sbase + size_t(min(n0 + 16 * nb + r, p.N - 1)) * p.groups + g;
-                float scale;
-                uint32_t z = 8;
-                if constexpr (E2M1) {
-                    scale = e8m0_value(p.S[si]);
-                } else {
-                    scale = scale16<BF16>(reinterpret_cast<const uint16_t *>(p.S)[si]);
-                    if (p.Z)
-                        z = p.Z[si];
-                }
-                const uint32_t zz = (0x6400u + z) * 0x10001u;   // 1024 + z, twice (z below 256: no carry)
-                f32x4 part[MB];
+                // 2^(ex - 127), ex = 255 converting to NaN.  Weights above 2 times
+                // the largest two would pass bf16's range: those blocks are
+                // multiplied unscaled, one lane group at a time, and their sums
+                // scaled afterwards.
+                const uint32_t ex = scale_of(st, t, nb, q, false);
+                const bool big = ex == 253 || ex == 254;
+                scale[nb] = __builtin_bit_cast(float, ex << 23);
+                if (__any(big)) {
+                    for (int g = 0; g < 4; ++g) {
+                        const uint32_t exg = __shfl(ex, 16 * g + r);
+                        const bool bigg = exg == 253 || exg == 254;
 #pragma unroll
-                for (int mb = 0; mb < MB; ++mb)
-                    part[mb] = f32x4{};
+                        for (int mb = 0; mb < MB; ++mb) {
+                            f32x4 part = {};
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    const uint32_t d = w[nb][kPer * s + j];
-                    u32x4 v;
-                    if constexpr (E2M1)
-                        v = e2m1_values<BF16>(d);
-                    else
-                        v = u4_values<BF16>(d, zz);
+                            for (int j = 0; j < 4; ++j) {
+                                const u32x4 v = e2m1_values<BF16>(big && q == g ? w[slot][nb][j] : 0, 1.0f);
+                                part = mfma_16x16x32<BF16>(piece(st, mb, j), v, part);
+                            }
 #pragma unroll
-                    for (int mb = 0; mb < MB; ++mb)
-                        part[mb] = mfma_16x16x32<BF16>(a[mb][kPer * s + j], v, part[mb]);
-                }
-#pragma unroll
-                for (int mb = 0; mb < MB; ++mb) {
-                    if constexpr (BF16 && !E2M1) {
-                        const float zs = 1.0f + float(z) * 0.0625f;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[nb][mb][i] = __builtin_fmaf(scale * 16.0f, __builtin_fmaf(-zs, asum[mb][i], part[mb][i]),
-                                                            acc[nb][mb][i]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[nb][mb][i] = __builtin_fmaf(scale, part[mb][i], acc[nb][mb][i]);
+                            for (int i = 0; i < 4; ++i)
+                                acc[nb][mb][i] += bigg ? e8m0_value(exg) * part[i] : 0.0f;
+                        }
                     }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        w[slot][nb][j] = big ? 0 : w[slot][nb][j];
                 }
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                u32x4 av[MB];
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb)
+                    av[mb] = piece(st, mb, j);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    const u32x4 v = e2m1_values<BF16>(w[slot][nb][j], scale[nb]);
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb)
+                        acc[nb][mb] = mfma_16x16x32<BF16>(av[mb], v, acc[nb][mb]);
+                }
+            }
+            return;
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+            w4_arrange<SPAN>(w[slot][nb]);
+#pragma unroll
+        for (int s = 0; s < kSpans; ++s) {
+            f32x4 part[NB][MB], sum[MB];
+            uint32_t zz[NB];
+            float scale[NB], zero[NB];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const uint32_t b = scale_of(st, t, nb, s, false);
+                if constexpr (E2M1) {
+                    scale[nb] = e8m0_value(b);
+                } else {
+                    scale[nb] = scale16<BF16>(uint16_t(b));
+                    zero[nb] = p.Z ? float(scale_of(st, t, nb, s, true)) : 8.0f;
+                    zz[nb] = 0;
+                    if constexpr (!BF16)
+                        zz[nb] = __builtin_bit_cast(uint16_t, _Float16(zero[nb])) * 0x10001u;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                u32x4 av[MB];
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb) {
+                    av[mb] = piece(st, mb, kPer * s + j);
+                    // the rows' sums over the span, the same in every column
+                    if constexpr (kSums)
+                        sum[mb] = mfma_16x16x32<BF16>(av[mb], ones, j ? sum[mb] : f32x4{});
+                }
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    const uint32_t d = w[slot][nb][kPer * s + j];
+                    u32x4 v;
+                    if constexpr (E2M1)
+                        v = e2m1_values<BF16>(d, 1.0f);
+                    else
+                        v = u4_values<BF16>(d, zz[nb]);
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb)
+                        part[nb][mb] = mfma_16x16x32<BF16>(av[mb], v, j ? part[nb][mb] : f32x4{});
+                }
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float v = kSums ? __builtin_fmaf(-zero[nb], sum[mb][i], part[nb][mb][i]) : part[nb][mb][i];
+                        acc[nb][mb][i] = __builtin_fmaf(scale[nb], v, acc[nb][mb][i]);
+                    }
+        }
+    };
+
+    // Step t: wait until its own loads have landed (the kAhead - 1 later steps'
+    // may stay in flight), barrier (every wave's copies are in LDS, and all
+    // have read the stage that is filled next), compute, load step t + kAhead.
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+        load(u, stage(u), u);
+        sched_fence();
+    }
+    for (int t0 = 0; t0 < steps; t0 += kStages) {
+#pragma unroll
+        for (int u = 0; u < kStages; ++u) {
+            if (t0 + u >= steps)
+                break;
+            lds_barrier_keep_vm<(kAhead - 1) * kLoads>();
+            sched_fence();
+            load((u + kAhead) % kStages, stage((u + kAhead) % kStages), t0 + u + kAhead);
+            sched_fence();
+            compute(stage(u), u, t0 + u);
+            sched_fence();
         }
     }
+    lds_barrier_keep_vm<0>();   // no copy may still be writing LDS below, or when the workgroup ends
 
-    // sums over waves: tile (nb, mb) is added up and stored by wave tile % 8;
-    // lane holds column r of the 16, rows 4q .. 4q+3
+    // sums over the KQ waves of a column block: tile tl of column block ng is
+    // added up, in wave order, by one of them (waves 0-3 leave theirs in stage
+    // 0, 4-7 in stage 1); lane holds column r of the 16, rows 4q .. 4q+3
+    auto sums = [&](int wv, int tl) {
+        return reinterpret_cast<f32x4 *>((wv < 4 ? st0 : st1) + (((wv & 3) * NB * MB + tl) * 64 + lane) * 16);
+    };
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
-            *reinterpret_cast<f32x4 *>(red[wave][nb * MB + mb][lane]) = acc[nb][mb];
+            *sums(wave, nb * MB + mb) = acc[nb][mb];
     __syncthreads();
-    for (int tl = wave; tl < kTiles; tl += kW4Waves) {
-        f32x4 sum = *reinterpret_cast<const f32x4 *>(red[0][tl][lane]);
+    for (int tl = kq; tl < NB * MB; tl += KQ) {
+        f32x4 sum = *sums(ng, tl);
 #pragma unroll
-        for (int w = 1; w < kW4Waves; ++w)
-            sum += *reinterpret_cast<const f32x4 *>(red[w][tl][lane]);
-        const int n = n0 + 16 * (tl / MB) + r, mb = tl % MB;
+        for (int x = 1; x < KQ; ++x)
+            sum += *sums(NG * x + ng, tl);
+        const int n = n0 + 16 * (NB * ng + tl / MB) + r, mb = tl % MB;
         if (n >= p.N)
             continue;
 #pragma unroll
@@ -297,46 +459,76 @@ w4_kernel(W4Kernel p)
             const int m = 16 * mb + 4 * q + i;
             if (m >= rows)
                 continue;
-            const size_t at = size_t(m0 + m) * p.ldd + n;
-            using T = std::conditional_t<OUT == kOutF32, float, std::conditional_t<OUT == kOutBf16, __bf16, _Float16>>;
-            T *d = static_cast<T *>(p.D) + at;
-            *d = T(p.beta ? sum[i] + float(*d) : sum[i]);
+            if constexpr (SPLIT) {
+                p.ws[(size_t(blockIdx.z) * p.M + m0 + m) * p.N + n] = sum[i];
+            } else {
+                const size_t at = size_t(m0 + m) * p.ldd + n;
+                using T = std::conditional_t<OUT == kOutF32, float, std::conditional_t<OUT == kOutBf16, __bf16, _Float16>>;
+                T *d = static_cast<T *>(p.D) + at;
+                *d = T(p.beta ? sum[i] + float(*d) : sum[i]);
+            }
         }
     }
 }
 
-template <bool BF16, bool E2M1, int SPAN, int MB, int NB>
+template <bool BF16, bool E2M1, int SPAN, int ROWS, int NB, int NG, bool SPLIT = false>
 hipError_t launch_w4_tile(const W4Args &a, hipStream_t stream)
 {
-    const W4Kernel p{static_cast<const uint8_t *>(a.A), a.B, static_cast<const uint8_t *>(a.S), a.Z, a.offsets, a.D,
-                     a.M, a.N, a.K, a.E, a.group, a.groups, a.lda, a.ldd, a.beta};
-    const int64_t tiles = a.offsets ? most_tiles(a.E, a.M, 16 * MB) : (a.M + 16 * MB - 1) / (16 * MB);
-    const dim3 grid((a.N + 16 * NB - 1) / (16 * NB), unsigned(tiles));
-    if (a.out == kOutF32)
-        hipLaunchKernelGGL((w4_kernel<BF16, E2M1, SPAN, MB, NB, kOutF32>), grid, dim3(64 * kW4Waves), 0, stream, p);
-    else
-        hipLaunchKernelGGL((w4_kernel<BF16, E2M1, SPAN, MB, NB, BF16 ? kOutBf16 : kOutF16>), grid, dim3(64 * kW4Waves), 0,
-                           stream, p);
+    constexpr int KQ = 8 / NG, kCols = 16 * NB * NG;
+    const int steps = (a.K + kChunk * KQ - 1) / (kChunk * KQ), part_steps = (steps + a.parts - 1) / a.parts;
+    const W4Kernel p{static_cast<const uint8_t *>(a.A), a.B, static_cast<const uint8_t *>(a.S), a.Z, a.offsets, a.D, a.ws,
+                     a.M, a.N, a.K, a.E, (uint64_t(1) << 32) / unsigned(a.group < kChunk ? 1 : a.group / kChunk) + 1,
+                     a.groups, a.lda, a.ldd, a.beta, part_steps};
+    const int64_t tiles = a.offsets ? most_tiles(a.E, a.M, ROWS) : (a.M + ROWS - 1) / ROWS;
+    const dim3 grid((a.N + kCols - 1) / kCols, unsigned(tiles), SPLIT ? (steps + part_steps - 1) / part_steps : 1);
+    constexpr int kNarrow = BF16 ? kOutBf16 : kOutF16;
+    if constexpr (SPLIT) {
+        hipLaunchKernelGGL((w4_kernel<BF16, E2M1, SPAN, ROWS, NB, NG, kOutF32, true>), grid, dim3(kW4Threads), 0, stream, p);
+    } else if (a.out == kOutF32) {
+        hipLaunchKernelGGL((w4_kernel<BF16, E2M1, SPAN, ROWS, NB, NG, kOutF32, false>), grid, dim3(kW4Threads), 0, stream, p);
+    } else {
+        hipLaunchKernelGGL((w4_kernel<BF16, E2M1, SPAN, ROWS, NB, NG, kNarrow, false>), grid, dim3(kW4Threads), 0, stream, p);
+    }
     return hipGetLastError();
 }
 
+#ifndef W4_TUNE
 template <bool BF16, bool E2M1, int SPAN>
 hipError_t launch_w4_span(const W4Args &a, hipStream_t stream)
 {
-    return a.M <= 16 || (a.offsets && a.M <= 16 * int64_t(a.E)) ? launch_w4_tile<BF16, E2M1, SPAN, 1, 2>(a, stream)
-                                                               : launch_w4_tile<BF16, E2M1, SPAN, 4, 2>(a, stream);
+    // Columns of a workgroup: as many as leave enough workgroups, since more
+    // columns share a copy of A and make a wave's part of K, and with it its
+    // run of steps, longer (16 rows by 16384 x 8192: 18.5 us with 64 columns,
+    // 24.6 with 32; one row by 4096 x 4096: 6.7 us with 32, 4.8 with 16)
+    const int64_t tiles = a.E ? (a.E < a.M ? a.E : a.M) : 1;
+    auto enough = [&](int cols, int wgs) { return tiles * ((a.N + cols - 1) / cols) >= wgs; };
+    switch (w4_rows(a)) {
+    case 4:
+        return enough(128, 512)  ? launch_w4_tile<BF16, E2M1, SPAN, 4, 2, 4>(a, stream)
+               : enough(32, 256) ? launch_w4_tile<BF16, E2M1, SPAN, 4, 2, 1>(a, stream)
+                                 : launch_w4_tile<BF16, E2M1, SPAN, 4, 1, 1>(a, stream);
+    case 16:
+        return enough(128, 512)  ? launch_w4_tile<BF16, E2M1, SPAN, 16, 2, 4>(a, stream)
+               : enough(64, 256) ? launch_w4_tile<BF16, E2M1, SPAN, 16, 2, 2>(a, stream)
+               : enough(32, 256) ? launch_w4_tile<BF16, E2M1, SPAN, 16, 1, 2>(a, stream)
+                                 : launch_w4_tile<BF16, E2M1, SPAN, 16, 1, 1>(a, stream);
+    default:
+        return a.parts > 1 ? launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 4, true>(a, stream)
+                           : launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 4>(a, stream);
+    }
 }
+#endif
 
 template <bool BF16, bool E2M1>
 hipError_t launch_w4_kind(const W4Args &a, hipStream_t stream)
 {
-    if constexpr (!E2M1) {
+    if constexpr (E2M1) {
+        return launch_w4_span<BF16, E2M1, BF16 ? 128 : 32>(a, stream);
+    } else {
         if (a.group % 128 == 0)
             return launch_w4_span<BF16, E2M1, 128>(a, stream);
-        if (a.group == 64)
-            return launch_w4_span<BF16, E2M1, 64>(a, stream);
+        return a.group == 64 ? launch_w4_span<BF16, E2M1, 64>(a, stream) : launch_w4_span<BF16, E2M1, 32>(a, stream);
     }
-    return launch_w4_span<BF16, E2M1, 32>(a, stream);
 }
 
 }  // namespace
