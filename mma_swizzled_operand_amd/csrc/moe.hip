@@ -17,9 +17,10 @@ namespace mswz {
 namespace {
 
 constexpr int kSortThreads = 256, kSortWaves = kSortThreads / 64;
-constexpr int kRounds = 8;                                  // choices per lane
+constexpr int kRounds = 4;                                  // choices per lane
 constexpr int kSlots = kSortThreads * kRounds;              // choices per workgroup of the sort
 constexpr int kMaxE = 1024;
+constexpr int kFew = 1024;                                  // choices that one launch sorts and copies
 
 // Lanes that hold the same key, as a mask: one ballot per key bit.
 __device__ __forceinline__ uint64_t same_key(uint32_t key, int bits)
@@ -33,7 +34,7 @@ __device__ __forceinline__ uint64_t same_key(uint32_t key, int bits)
 }
 
 // The sort's common part.  Wave w of workgroup g owns choices
-// kSlots g + 512 w .. +511, 64 per round in choice order.  rank[r] is the
+// kSlots g + 64 kRounds w .., 64 per round in choice order.  rank[r] is the
 // number of the wave's earlier choices of the same expert, hist[w][e] the
 // wave's count.  Choices left out and places beyond n count as expert E,
 // which has no row of hist.
@@ -83,37 +84,61 @@ moe_count_kernel(const int32_t *__restrict__ ids, int n, int E, int32_t *__restr
 
 // Places of a workgroup's choices: the counts of all workgroups give each
 // expert's first row and what earlier workgroups put before this one's
-// choices, the waves' own counts the rest.
+// choices, the waves' own counts the rest.  Each workgroup adds the counts up
+// for itself (from L2), kParts threads an expert, eight loads of each in
+// flight: one load at a time took 20 us at 32 workgroups.
 __global__ void __launch_bounds__(kSortThreads)
 moe_place_kernel(const int32_t *__restrict__ ids, int n, int E, int bits, const int32_t *__restrict__ counts,
                  int32_t *__restrict__ offsets, int32_t *__restrict__ order, int32_t *__restrict__ pos)
 {
     __shared__ int32_t hist[kSortWaves][kMaxE];
-    __shared__ int32_t base[kMaxE];
+    __shared__ int32_t total[kMaxE], base[kMaxE];
     __shared__ int32_t wave_sum[kSortWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, groups = gridDim.x;
-    for (int e = tid; e < kSortWaves * kMaxE; e += kSortThreads)
-        (&hist[0][0])[e] = 0;
+    for (int e = tid; e < E; e += kSortThreads) {
+        total[e] = base[e] = 0;
+        for (int w = 0; w < kSortWaves; ++w)
+            hist[w][e] = 0;
+    }
     __syncthreads();
+    {
+        // experts in columns of `width` threads, groups dealt to the rows of threads
+        int width = 64;
+        while (width < E && width < kSortThreads)
+            width *= 2;
+        const int parts = kSortThreads / width, part = tid / width;
+        for (int e = tid % width; e < E; e += width) {
+            int sum = 0, before = 0;
+            for (int g0 = part; g0 < groups; g0 += 8 * parts) {
+                int c[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    c[i] = counts[int64_t(min(g0 + i * parts, groups - 1)) * E + e];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int g = g0 + i * parts;
+                    sum += g < groups ? c[i] : 0;
+                    before += g < int(blockIdx.x) ? c[i] : 0;
+                }
+            }
+            atomicAdd(&total[e], sum);
+            atomicAdd(&base[e], before);
+        }
+    }
     uint32_t key[kRounds];
     int rank[kRounds];
     const int first = blockIdx.x * kSlots + wave * 64 * kRounds;
     wave_ranks(ids, n, E, bits, first, hist[wave], lane, key, rank);
+    __syncthreads();
 
-    // each thread: up to four consecutive experts' totals, then a scan over threads
+    // each thread: consecutive experts' totals, then a scan over threads
     constexpr int kPer = kMaxE / kSortThreads;
-    int total[kPer], before[kPer], sum = 0;
+    const int per = (E + kSortThreads - 1) / kSortThreads;
+    int mine[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int e = tid * kPer + i;
-        total[i] = before[i] = 0;
-        if (e < E)
-            for (int g = 0; g < groups; ++g) {
-                const int c = counts[int64_t(g) * E + e];
-                total[i] += c;
-                before[i] += g < int(blockIdx.x) ? c : 0;
-            }
-        sum += total[i];
+        mine[i] = i < per && tid * per + i < E ? total[tid * per + i] : 0;
+        sum += mine[i];
     }
     const int scan = wave_scan(sum, lane);
     if (lane == 63)
@@ -127,17 +152,16 @@ moe_place_kernel(const int32_t *__restrict__ ids, int n, int E, int bits, const 
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int e = tid * kPer + i;
-        if (e < E) {
-            base[e] = start + before[i];
-            if (blockIdx.x == 0) {
+        const int e = tid * per + i;
+        if (i < per && e < E) {
+            base[e] += start;
+            if (blockIdx.x == 0)
                 offsets[e] = start;
-                if (e == E - 1)
-                    offsets[E] = start + total[i];
-            }
         }
-        start += total[i];
+        start += mine[i];
     }
+    if (blockIdx.x == 0 && tid == 0)
+        offsets[E] = used;
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
@@ -156,6 +180,95 @@ moe_place_kernel(const int32_t *__restrict__ ids, int n, int E, int bits, const 
         if (slot >= used)
             order[slot] = -1;
     }
+}
+
+// Few choices: the sort and the copy in one launch.  Workgroup (t, piece)
+// finds the rows of token t's choices by counting the choices before them
+// (smaller expert, or the same expert earlier), all of them from one read of
+// ids, and copies its piece of the row; workgroup T writes offsets and the
+// places behind the last group, from a histogram.
+__global__ void __launch_bounds__(256)
+moe_few_kernel(const int32_t *__restrict__ ids, const u32x4 *__restrict__ X, u32x4 *__restrict__ Xs, int T, int topk,
+               int E, int vecs, int64_t ldx16, int32_t *__restrict__ offsets, int32_t *__restrict__ order,
+               int32_t *__restrict__ pos)
+{
+    __shared__ int32_t cnt[kMaxE];
+    __shared__ int32_t wave_sum[4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = T * topk;
+    const int t = blockIdx.x;
+    if (t < T) {
+        for (int j = tid; j < topk; j += 256)
+            cnt[j] = 0;
+        __syncthreads();
+        constexpr int kPer = kFew / 256;
+        uint32_t id[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int s = tid + 256 * i;
+            id[i] = s < n ? uint32_t(ids[s]) : ~0u;
+        }
+        for (int j = 0; j < topk; ++j) {
+            const int slot = t * topk + j;
+            const uint32_t mine = uint32_t(ids[slot]);
+            int before = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                before += __builtin_popcountll(__ballot(id[i] < mine || (id[i] == mine && tid + 256 * i < slot)));
+            if (lane == 0 && before)
+                atomicAdd(&cnt[j], before);
+        }
+        __syncthreads();
+        if (blockIdx.y == 0)
+            for (int j = tid; j < topk; j += 256) {
+                const int slot = t * topk + j;
+                const bool in = uint32_t(ids[slot]) < uint32_t(E);
+                pos[slot] = in ? cnt[j] : -1;
+                if (in)
+                    order[cnt[j]] = slot;
+            }
+        const int v = blockIdx.y * 256 + tid;
+        if (X && v < vecs) {
+            const u32x4 x = X[t * ldx16 + v];
+            for (int j = 0; j < topk; ++j)
+                if (uint32_t(ids[t * topk + j]) < uint32_t(E))
+                    Xs[int64_t(cnt[j]) * vecs + v] = x;
+        }
+        return;
+    }
+    if (blockIdx.y)
+        return;
+    for (int e = tid; e < E; e += 256)
+        cnt[e] = 0;
+    __syncthreads();
+    for (int s = tid; s < n; s += 256) {
+        const uint32_t id = uint32_t(ids[s]);
+        if (id < uint32_t(E))
+            atomicAdd(&cnt[id], 1);
+    }
+    __syncthreads();
+    const int per = (E + 255) / 256;
+    int sum = 0;
+    for (int i = 0; i < per; ++i)
+        sum += tid * per + i < E ? cnt[tid * per + i] : 0;
+    const int scan = wave_scan(sum, lane);
+    if (lane == 63)
+        wave_sum[wave] = scan;
+    __syncthreads();
+    int start = scan - sum, used = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        start += w < wave ? wave_sum[w] : 0;
+        used += wave_sum[w];
+    }
+    for (int i = 0; i < per; ++i)
+        if (tid * per + i < E) {
+            offsets[tid * per + i] = start;
+            start += cnt[tid * per + i];
+        }
+    if (tid == 0)
+        offsets[E] = used;
+    for (int s = used + tid; s < n; s += 256)
+        order[s] = -1;
 }
 
 // Xs[pos[t][j]] = X[t]: one wave per token and 1 KiB column piece.
@@ -200,13 +313,16 @@ struct Row16 {
 };
 
 // Y[t] = sum_j w Ys[pos]: one wave per token and 1 KiB column piece; the sum is
-// held in fp32 and rounded once.
+// held in fp32 and rounded once.  The rows of kJ choices are loaded before any
+// is added, so that their latencies run together (one after the other, 4096
+// tokens of 8 x 2048 bf16 took 41.5 us).
 template <int DT, bool WEIGHTS>
 __global__ void __launch_bounds__(256)
 moe_combine_kernel(const u32x4 *__restrict__ Ys, const int32_t *__restrict__ pos, const float *__restrict__ w,
                    u32x4 *__restrict__ Y, int T, int topk, int vecs, int pieces, int64_t ldx16)
 {
     using R = Row16<DT>;
+    constexpr int kJ = 8;
     const int lane = threadIdx.x & 63;
     const int64_t id = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t = int(id / pieces), v = int(id % pieces) * 64 + lane;
@@ -214,16 +330,27 @@ moe_combine_kernel(const u32x4 *__restrict__ Ys, const int32_t *__restrict__ pos
         return;
     const uint32_t rows = uint32_t(T) * uint32_t(topk);
     float acc[R::kElems] = {};
-    for (int j = 0; j < topk; ++j) {
-        const uint32_t p = uint32_t(pos[int64_t(t) * topk + j]);
-        if (p >= rows)
-            continue;
-        float y[R::kElems];
-        R::get(Ys[int64_t(p) * vecs + v], y);
-        const float wj = WEIGHTS ? w[int64_t(t) * topk + j] : 1.0f;
+    for (int j0 = 0; j0 < topk; j0 += kJ) {
+        u32x4 y[kJ];
+        uint32_t p[kJ];
 #pragma unroll
-        for (int i = 0; i < R::kElems; ++i)
-            acc[i] = WEIGHTS ? __builtin_fmaf(wj, y[i], acc[i]) : acc[i] + y[i];
+        for (int j = 0; j < kJ; ++j)
+            p[j] = j0 + j < topk ? uint32_t(pos[int64_t(t) * topk + j0 + j]) : ~0u;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j)
+            if (p[j] < rows)
+                y[j] = Ys[int64_t(p[j]) * vecs + v];
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+            if (p[j] >= rows)
+                continue;
+            float f[R::kElems];
+            R::get(y[j], f);
+            const float wj = WEIGHTS ? w[int64_t(t) * topk + j0 + j] : 1.0f;
+#pragma unroll
+            for (int i = 0; i < R::kElems; ++i)
+                acc[i] = WEIGHTS ? __builtin_fmaf(wj, f[i], acc[i]) : acc[i] + f[i];
+        }
     }
     Y[t * ldx16 + v] = R::put(acc);
 }
@@ -293,15 +420,23 @@ int bits_for(int E)
 
 }  // namespace
 
+static bool few(const MoeArgs &a) { return a.T * a.topk <= kFew && a.topk <= kMaxE; }
+
 int64_t moe_workspace_bytes(const MoeArgs &a)
 {
     const int64_t n = int64_t(a.T) * a.topk;
-    return (n + kSlots - 1) / kSlots * a.E * 4;
+    return few(a) ? 0 : (n + kSlots - 1) / kSlots * a.E * 4;
 }
 
 hipError_t launch_moe_dispatch(const MoeArgs &a, const int32_t *ids, const void *X, void *Xs, int32_t *offsets,
                                int32_t *order, int32_t *pos, void *workspace, hipStream_t stream)
 {
+    if (few(a)) {
+        hipLaunchKernelGGL(moe_few_kernel, dim3(a.T + 1, X ? (a.vecs + 255) / 256 : 1), dim3(256), 0, stream, ids,
+                           static_cast<const u32x4 *>(X), static_cast<u32x4 *>(Xs), a.T, a.topk, a.E, a.vecs, a.ldx16,
+                           offsets, order, pos);
+        return hipGetLastError();
+    }
     const int n = a.T * a.topk, groups = (n + kSlots - 1) / kSlots;
     int32_t *counts = static_cast<int32_t *>(workspace);
     hipLaunchKernelGGL(moe_count_kernel, dim3(groups), dim3(kSortThreads), 0, stream, ids, n, a.E, counts);

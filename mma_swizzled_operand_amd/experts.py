@@ -105,10 +105,11 @@ class W4Plan(_Plan):
         matrices = max(1, self.E)
         self.b_numel = matrices * self.N * (self.K // 2)
         self.s_numel = matrices * self.N * (-(-self.K // self.group))
+        self.ws_bytes, self._run = int(self._lib.gemm_w4_plan_workspace_size(self._h)), self._lib.gemm_run_w4
 
     def workspace_bytes(self) -> int:
         """Device workspace gemm_run_w4 needs for this plan (0: none)."""
-        return int(self._lib.gemm_w4_plan_workspace_size(self.handle))
+        return self.ws_bytes
 
 
 class GroupedPlan(_Plan):
@@ -126,6 +127,7 @@ class GroupedPlan(_Plan):
         self.a_numel = self.M * self.K
         self.b_numel = self.K * self.N * (1 if axis == "k" else self.E)
         self.d_numel = self.M * self.N * (self.E if axis == "k" else 1)
+        self._run = self._lib.gemm_run_grouped
 
 
 class MoePlan(_Plan):
@@ -137,10 +139,13 @@ class MoePlan(_Plan):
         self._create(self.T, self.topk, self.E, self.H, _dt(dt), int(ldx))
         self.dt, self.ldx, self.type = dt, int(ldx) or self.H, _TORCH[dt]
         self.choices = self.T * self.topk
+        self.ws_bytes = int(self._lib.moe_plan_workspace_size(self._h))
+        self._dispatch, self._combine = self._lib.moe_dispatch, self._lib.moe_combine
+        self._combine_grad = self._lib.moe_combine_grad
 
     def workspace_bytes(self) -> int:
         """Device workspace moe_dispatch needs for this plan (0: none)."""
-        return int(self._lib.moe_plan_workspace_size(self.handle))
+        return self.ws_bytes
 
 
 def gemm_w4_plan_create(M, N, K, a_dt="bf16", w_dt="u4", d_dt="bf16", group=128, experts=0, lda=0, ldd=0) -> W4Plan:
@@ -162,10 +167,10 @@ def moe_plan_create(T, topk, E, H, dt="bf16", ldx=0) -> MoePlan:
 
 def _packed(t, dtype, numel, dev, name):
     """Device pointer of a contiguous tensor of ``numel`` elements on GPU ``dev``."""
-    if t.dtype != dtype or t.numel() != numel or not t.is_contiguous() or t.get_device() != dev:
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {numel} elements on GPU {dev}, got "
-                         f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.numel() == numel and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {numel} elements on GPU {dev}, got "
+                     f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
 def _rows(t, dtype, rows, cols, ld, dev, name):
@@ -182,20 +187,21 @@ def _rows(t, dtype, rows, cols, ld, dev, name):
 
 def _workspace(t, need, dev):
     if not need:
-        return None, 0
+        return None
     if t is None:
         raise ValueError(f"workspace: the plan needs {need} bytes")
-    size = t.numel() * t.element_size()
-    if size < need or not t.is_contiguous() or t.get_device() != dev:
-        raise ValueError(f"workspace: expected a contiguous tensor of at least {need} bytes on GPU {dev}, got {size} "
-                         f"bytes on {t.device}")
-    return t.data_ptr(), size
+    if t.numel() * t.element_size() >= need and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    raise ValueError(f"workspace: expected a contiguous tensor of at least {need} bytes on GPU {dev}, got "
+                     f"{t.numel() * t.element_size()} bytes on {t.device}")
 
 
 def _device(plan, kind, t, name):
-    """The GPU that tensor ``t`` lives on, after checking the plan's class."""
+    """The GPU that tensor ``t`` lives on, after checking the plan."""
     if not isinstance(plan, kind):
         raise TypeError(f"expected a {kind.__name__}, got {type(plan).__name__}")
+    if plan._h is None:
+        raise ValueError("plan has been destroyed")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
     dev = t.get_device()
@@ -204,21 +210,25 @@ def _device(plan, kind, t, name):
     return dev
 
 
+# The handle of torch's current stream of a GPU.  (torch.cuda.current_stream
+# makes a stream object first: 1.1 us of a call that takes 6.)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _call(fn, what, dev, stream, *args):
     """Call a run function with the stream's handle last, on GPU ``dev``."""
     if stream is None:
-        st = torch.cuda.current_stream(dev).cuda_stream
-    elif isinstance(stream, int):
-        st = stream
-    else:
+        stream = _current_stream(dev)
+    elif not isinstance(stream, int):
         if stream.device.index != dev:
             raise ValueError(f"stream: on {stream.device}, the tensors are on GPU {dev}")
-        st = stream.cuda_stream
+        stream = stream.cuda_stream
     if torch.cuda.current_device() == dev:
-        rc = fn(*args, st)
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, st)
+            rc = fn(*args, stream)
     if rc != 0:
         from . import MswzError
         raise MswzError(rc, what)
@@ -232,21 +242,20 @@ def gemm_run_w4(plan: W4Plan, A, B, S, D, Z=None, offsets=None, beta: int = 0, w
         raise ValueError("offsets: given exactly for a plan with experts")
     if Z is not None and plan.w_dt != "u4":
         raise ValueError("Z: only u4 weights have zero points")
-    need = plan.workspace_bytes()
-    ws, size = _workspace(workspace, need, dev)
-    _call(plan._lib.gemm_run_w4, "gemm_run_w4", dev, stream, plan.handle,
+    _call(plan._run, "gemm_run_w4", dev, stream, plan._h,
           _rows(A, plan.a_type, plan.M, plan.K, plan.lda, dev, "A"),
           _packed(B, torch.uint8, plan.b_numel, dev, "B"), _packed(S, plan.s_type, plan.s_numel, dev, "S"),
           None if Z is None else _packed(Z, torch.uint8, plan.s_numel, dev, "Z"),
           None if offsets is None else _packed(offsets, torch.int32, plan.E + 1, dev, "offsets"),
-          _rows(D, plan.d_type, plan.M, plan.N, plan.ldd, dev, "D"), int(beta), ws, size)
+          _rows(D, plan.d_type, plan.M, plan.N, plan.ldd, dev, "D"), int(beta),
+          _workspace(workspace, plan.ws_bytes, dev), plan.ws_bytes)
 
 
 def gemm_run_grouped(plan: GroupedPlan, A, B, offsets, D, beta: int = 0, stream=None) -> None:
     """Enqueue the grouped product (axis "m": A [M][K], B [E][N][K] or [E][K][N], D [M][N]; axis "k": A [K][M],
     B [K][N], D [E][M][N])."""
     dev = _device(plan, GroupedPlan, A, "A")
-    _call(plan._lib.gemm_run_grouped, "gemm_run_grouped", dev, stream, plan.handle,
+    _call(plan._run, "gemm_run_grouped", dev, stream, plan._h,
           _packed(A, plan.type, plan.a_numel, dev, "A"), _packed(B, plan.type, plan.b_numel, dev, "B"),
           _packed(offsets, torch.int32, plan.E + 1, dev, "offsets"),
           _packed(D, plan.d_type, plan.d_numel, dev, "D"), int(beta))
@@ -259,19 +268,18 @@ def moe_dispatch(plan: MoePlan, ids, X, Xs, offsets, order, pos, workspace=None,
     if (X is None) != (Xs is None):
         raise ValueError("X and Xs: both or neither")
     n = plan.choices
-    ws, size = _workspace(workspace, plan.workspace_bytes(), dev)
-    _call(plan._lib.moe_dispatch, "moe_dispatch", dev, stream, plan.handle, _packed(ids, torch.int32, n, dev, "ids"),
+    _call(plan._dispatch, "moe_dispatch", dev, stream, plan._h, _packed(ids, torch.int32, n, dev, "ids"),
           None if X is None else _rows(X, plan.type, plan.T, plan.H, plan.ldx, dev, "X"),
           None if X is None else _packed(Xs, plan.type, n * plan.H, dev, "Xs"),
           _packed(offsets, torch.int32, plan.E + 1, dev, "offsets"), _packed(order, torch.int32, n, dev, "order"),
-          _packed(pos, torch.int32, n, dev, "pos"), ws, size)
+          _packed(pos, torch.int32, n, dev, "pos"), _workspace(workspace, plan.ws_bytes, dev), plan.ws_bytes)
 
 
 def moe_combine(plan: MoePlan, Ys, pos, Y, weights=None, stream=None) -> None:
     """Enqueue Y[t] = sum_j weights[t][j] Ys[pos[t][j]] (weights None: ones, the gradient of moe_dispatch)."""
     dev = _device(plan, MoePlan, Ys, "Ys")
     n = plan.choices
-    _call(plan._lib.moe_combine, "moe_combine", dev, stream, plan.handle,
+    _call(plan._combine, "moe_combine", dev, stream, plan._h,
           _packed(Ys, plan.type, n * plan.H, dev, "Ys"), _packed(pos, torch.int32, n, dev, "pos"),
           None if weights is None else _packed(weights, torch.float32, n, dev, "weights"),
           _rows(Y, plan.type, plan.T, plan.H, plan.ldx, dev, "Y"))
@@ -281,7 +289,7 @@ def moe_combine_grad(plan: MoePlan, dY, Ys, pos, weights, dYs, dw, stream=None) 
     """Enqueue moe_combine's gradients: dYs[pos[t][j]] = weights[t][j] dY[t] and dw[t][j] = <dY[t], Ys[pos[t][j]]>."""
     dev = _device(plan, MoePlan, dY, "dY")
     n = plan.choices
-    _call(plan._lib.moe_combine_grad, "moe_combine_grad", dev, stream, plan.handle,
+    _call(plan._combine_grad, "moe_combine_grad", dev, stream, plan._h,
           _rows(dY, plan.type, plan.T, plan.H, plan.ldx, dev, "dY"), _packed(Ys, plan.type, n * plan.H, dev, "Ys"),
           _packed(pos, torch.int32, n, dev, "pos"), _packed(weights, torch.float32, n, dev, "weights"),
           _packed(dYs, plan.type, n * plan.H, dev, "dYs"), _packed(dw, torch.float32, n, dev, "dw"))
