@@ -186,9 +186,6 @@ int moe_plan_create(moe_plan **out, int64_t T, int64_t topk, int64_t E, int64_t 
     const int64_t per16 = dt == MSWZ_DT_F32 ? 4 : 8;   // elements in 16 bytes
     if (H % per16 != 0 || ldx % per16 != 0 || ldx > kMaxLd)
         return MSWZ_ERR_UNSUPPORTED;
-    // one wave per token and 1 KiB piece of its row
-    if (T * ((H / per16 + 63) / 64) >= int64_t(1) << 31)
-        return MSWZ_ERR_UNSUPPORTED;
     moe_plan *p = new (std::nothrow) moe_plan{};
     if (!p)
         return MSWZ_ERR_INVALID;

@@ -271,21 +271,59 @@ moe_few_kernel(const int32_t *__restrict__ ids, const u32x4 *__restrict__ X, u32
         order[s] = -1;
 }
 
-// Xs[pos[t][j]] = X[t]: one wave per token and 1 KiB column piece.
+// The values of choices j0 .. j0 + J - 1 of token t, J scalar loads at once
+// (behind the last choice its value again).
+template <int J, typename T>
+__device__ __forceinline__ void choices(const T *__restrict__ x, int64_t t, int topk, int j0, T *v)
+{
+    const T *const p = x + t * topk + j0;
+    if (j0 + J <= topk) {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            v[j] = p[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            v[j] = p[min(j, topk - 1 - j0)];
+    }
+}
+
+// A wave's token and first 16-byte piece: a workgroup's four waves share a row
+// of four or more 1 KiB pieces, shorter rows go one or two waves a token.
+// (Dividing a wave number by the row's pieces, in 64 bits, took more
+// instructions than the copy itself.)
+struct WaveRow {
+    int t, v;
+};
+__device__ __forceinline__ WaveRow wave_row(int lg)
+{
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    const int t = int((blockIdx.x * 4u + unsigned(wave)) >> lg);
+    return {t, (int(blockIdx.y) * 4 + (wave & ((1 << lg) - 1))) * 64 + (int(threadIdx.x) & 63)};
+}
+
+// Xs[pos[t][j]] = X[t]: one wave per token and 1 KiB column piece.  Stored past
+// the caches: with plain stores the rows' lines had to leave the memory-side
+// cache again while the copy (or the sum that follows it) read
+// (8192 tokens to 8 experts each, 2048 bf16: 59.4 -> 51.9 us; the sum of 4096
+// such tokens after its gradient 40.2 -> 27.6 us, of which the stores in the
+// gradient 10 and the sum's own 2.6).
+template <int J>
 __global__ void __launch_bounds__(256)
 moe_gather_kernel(const u32x4 *__restrict__ X, const int32_t *__restrict__ pos, u32x4 *__restrict__ Xs, int T, int topk,
-                  int vecs, int pieces, int64_t ldx16)
+                  int vecs, int lg, int64_t ldx16)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t id = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int t = int(id / pieces), v = int(id % pieces) * 64 + lane;
+    const auto [t, v] = wave_row(lg);
     if (t >= T || v >= vecs)
         return;
     const u32x4 x = X[t * ldx16 + v];
-    for (int j = 0; j < topk; ++j) {
-        const int p = pos[int64_t(t) * topk + j];
-        if (p >= 0)
-            Xs[int64_t(p) * vecs + v] = x;
+    for (int j0 = 0; j0 < topk; j0 += J) {
+        int p[J];
+        choices<J>(pos, t, topk, j0, p);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (p[j] >= 0 && j0 + j < topk)
+                __builtin_nontemporal_store(x, &Xs[int64_t(p[j]) * vecs + v]);
     }
 }
 
@@ -313,101 +351,110 @@ struct Row16 {
 };
 
 // Y[t] = sum_j w Ys[pos]: one wave per token and 1 KiB column piece; the sum is
-// held in fp32 and rounded once.  The rows of kJ choices are loaded before any
-// is added, so that their latencies run together (one after the other, 4096
-// tokens of 8 x 2048 bf16 took 41.5 us).
-template <int DT, bool WEIGHTS>
+// held in fp32 and rounded once.  The rows of J choices are loaded before any
+// is added, so that their latencies run together; a choice left out loads row
+// 0 and is masked, as a branch around a load made each wait for the one before
+// (4096 tokens of 8 x 2048 bf16 take 27.6 us, 150 MB at 5.4 TB/s).
+template <int DT, bool WEIGHTS, int J>
 __global__ void __launch_bounds__(256)
 moe_combine_kernel(const u32x4 *__restrict__ Ys, const int32_t *__restrict__ pos, const float *__restrict__ w,
-                   u32x4 *__restrict__ Y, int T, int topk, int vecs, int pieces, int64_t ldx16)
+                   u32x4 *__restrict__ Y, int T, int topk, int vecs, int lg, int64_t ldx16)
 {
     using R = Row16<DT>;
-    constexpr int kJ = 8;
-    const int lane = threadIdx.x & 63;
-    const int64_t id = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int t = int(id / pieces), v = int(id % pieces) * 64 + lane;
+    const auto [t, v] = wave_row(lg);
     if (t >= T || v >= vecs)
         return;
     const uint32_t rows = uint32_t(T) * uint32_t(topk);
     float acc[R::kElems] = {};
-    for (int j0 = 0; j0 < topk; j0 += kJ) {
-        u32x4 y[kJ];
-        uint32_t p[kJ];
+    for (int j0 = 0; j0 < topk; j0 += J) {
+        u32x4 y[J];
+        int p[J];
+        float wj[J];
+        choices<J>(pos, t, topk, j0, p);
+        if constexpr (WEIGHTS)
+            choices<J>(w, t, topk, j0, wj);
 #pragma unroll
-        for (int j = 0; j < kJ; ++j)
-            p[j] = j0 + j < topk ? uint32_t(pos[int64_t(t) * topk + j0 + j]) : ~0u;
+        for (int j = 0; j < J; ++j)
+            y[j] = Ys[int64_t(uint32_t(p[j]) < rows ? p[j] : 0) * vecs + v];
 #pragma unroll
-        for (int j = 0; j < kJ; ++j)
-            if (p[j] < rows)
-                y[j] = Ys[int64_t(p[j]) * vecs + v];
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-            if (p[j] >= rows)
-                continue;
+        for (int j = 0; j < J; ++j) {
+            const bool in = uint32_t(p[j]) < rows && j0 + j < topk;
             float f[R::kElems];
-            R::get(y[j], f);
-            const float wj = WEIGHTS ? w[int64_t(t) * topk + j0 + j] : 1.0f;
+            R::get(in ? y[j] : u32x4{}, f);
+            const float wi = !WEIGHTS ? 1.0f : in ? wj[j] : 0.0f;
 #pragma unroll
             for (int i = 0; i < R::kElems; ++i)
-                acc[i] = WEIGHTS ? __builtin_fmaf(wj, f[i], acc[i]) : acc[i] + f[i];
+                acc[i] = __builtin_fmaf(wi, f[i], acc[i]);
         }
     }
-    Y[t * ldx16 + v] = R::put(acc);
+    __builtin_nontemporal_store(R::put(acc), &Y[t * ldx16 + v]);
 }
 
 // dYs[pos] = w dY[t], dw = <dY[t], Ys[pos]>: one workgroup per token, its four
-// waves taking the row's 1 KiB pieces in turn; choices in groups of kJ, whose
-// dot products stay in registers and are summed over lanes, then waves, in a
-// fixed order.
-template <int DT>
+// waves taking the row's 1 KiB pieces in turn; choices in groups of J, loaded
+// as in the sum, whose dot products stay in registers and are summed over
+// lanes, then waves, in a fixed order.  (4096 tokens of 8 x 2048 bf16: 45.6 us,
+// 285 MB at 6.3 TB/s.)
+template <int DT, int J>
 __global__ void __launch_bounds__(256)
 moe_combine_grad_kernel(const u32x4 *__restrict__ dY, const u32x4 *__restrict__ Ys, const int32_t *__restrict__ pos,
                         const float *__restrict__ w, u32x4 *__restrict__ dYs, float *__restrict__ dw, int T, int topk,
                         int vecs, int64_t ldx16)
 {
     using R = Row16<DT>;
-    constexpr int kJ = 8;
-    __shared__ float part[4][kJ];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ float part[4][J];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t t = blockIdx.x;
     const uint32_t rows = uint32_t(T) * uint32_t(topk);
-    for (int j0 = 0; j0 < topk; j0 += kJ) {
-        float dot[kJ] = {};
-        for (int v = threadIdx.x; v < vecs; v += 256) {
-            float dy[R::kElems];
-            R::get(dY[t * ldx16 + v], dy);
+    for (int j0 = 0; j0 < topk; j0 += J) {
+        float dot[J] = {}, wj[J];
+        int p[J];
+        choices<J>(pos, t, topk, j0, p);
+        choices<J>(w, t, topk, j0, wj);
 #pragma unroll
-            for (int j = 0; j < kJ; ++j) {
-                if (j0 + j >= topk)
-                    break;
-                const uint32_t p = uint32_t(pos[t * topk + j0 + j]);
-                if (p >= rows)
-                    continue;
-                float y[R::kElems], g[R::kElems];
-                R::get(Ys[int64_t(p) * vecs + v], y);
-                const float wj = w[t * topk + j0 + j];
+        for (int j = 0; j < J; ++j)
+            p[j] = uint32_t(p[j]) < rows && j0 + j < topk ? p[j] : -1;
+        for (int v = tid; v < vecs; v += 256) {
+            float dy[R::kElems];
+            u32x4 y[J];
+            const u32x4 d = dY[t * ldx16 + v];
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                y[j] = __builtin_nontemporal_load(&Ys[int64_t(max(p[j], 0)) * vecs + v]);
+            R::get(d, dy);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                float f[R::kElems], g[R::kElems];
+                R::get(y[j], f);
 #pragma unroll
                 for (int i = 0; i < R::kElems; ++i) {
-                    dot[j] = __builtin_fmaf(dy[i], y[i], dot[j]);
-                    g[i] = wj * dy[i];
+                    dot[j] = __builtin_fmaf(dy[i], f[i], dot[j]);
+                    g[i] = wj[j] * dy[i];
                 }
-                dYs[int64_t(p) * vecs + v] = R::put(g);
+                if (p[j] >= 0)
+                    __builtin_nontemporal_store(R::put(g), &dYs[int64_t(p[j]) * vecs + v]);
             }
         }
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) {
+        for (int j = 0; j < J; ++j) {
 #pragma unroll
             for (int d = 32; d; d /= 2)
                 dot[j] += __shfl_xor(dot[j], d);
             if (lane == 0)
-                part[wave][j] = dot[j];
+                part[wave][j] = p[j] >= 0 ? dot[j] : 0.0f;
         }
         __syncthreads();
-        if (int(threadIdx.x) < kJ && j0 + int(threadIdx.x) < topk)
-            dw[t * topk + j0 + threadIdx.x] =
-                (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
+        if (tid < J && j0 + tid < topk)
+            dw[t * topk + j0 + tid] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
         __syncthreads();
     }
+}
+
+// waves that share a token's row (log2), and the grid of wave_row
+int waves_log2(const MoeArgs &a) { return a.vecs <= 64 ? 0 : a.vecs <= 128 ? 1 : 2; }
+dim3 row_grid(const MoeArgs &a, int lg)
+{
+    return dim3(unsigned(((int64_t(a.T) << lg) + 3) / 4), unsigned((a.vecs + 255) / 256));
 }
 
 int bits_for(int E)
@@ -443,29 +490,51 @@ hipError_t launch_moe_dispatch(const MoeArgs &a, const int32_t *ids, const void 
     hipLaunchKernelGGL(moe_place_kernel, dim3(groups), dim3(kSortThreads), 0, stream, ids, n, a.E, bits_for(a.E), counts,
                        offsets, order, pos);
     if (X) {
-        const int pieces = (a.vecs + 63) / 64;
-        const int64_t blocks = (int64_t(a.T) * pieces + 3) / 4;
-        hipLaunchKernelGGL(moe_gather_kernel, dim3(unsigned(blocks)), dim3(256), 0, stream, static_cast<const u32x4 *>(X),
-                           pos, static_cast<u32x4 *>(Xs), a.T, a.topk, a.vecs, pieces, a.ldx16);
+        const int lg = waves_log2(a);
+        const dim3 grid = row_grid(a, lg);
+        const auto *x = static_cast<const u32x4 *>(X);
+        auto *xs = static_cast<u32x4 *>(Xs);
+        if (a.topk <= 2)
+            hipLaunchKernelGGL(moe_gather_kernel<2>, grid, dim3(256), 0, stream, x, pos, xs, a.T, a.topk, a.vecs, lg, a.ldx16);
+        else
+            hipLaunchKernelGGL(moe_gather_kernel<8>, grid, dim3(256), 0, stream, x, pos, xs, a.T, a.topk, a.vecs, lg, a.ldx16);
     }
     return hipGetLastError();
 }
 
 namespace {
 
-template <int DT>
-hipError_t combine_dt(const MoeArgs &a, const void *Ys, const int32_t *pos, const float *w, void *Y, hipStream_t stream)
+template <int DT, int J>
+hipError_t combine_j(const MoeArgs &a, const void *Ys, const int32_t *pos, const float *w, void *Y, hipStream_t stream)
 {
-    const int pieces = (a.vecs + 63) / 64;
-    const int64_t blocks = (int64_t(a.T) * pieces + 3) / 4;
+    const int lg = waves_log2(a);
+    const dim3 grid = row_grid(a, lg);
     auto *y = static_cast<u32x4 *>(Y);
     auto *ys = static_cast<const u32x4 *>(Ys);
     if (w)
-        hipLaunchKernelGGL((moe_combine_kernel<DT, true>), dim3(unsigned(blocks)), dim3(256), 0, stream, ys, pos, w, y, a.T,
-                           a.topk, a.vecs, pieces, a.ldx16);
+        hipLaunchKernelGGL((moe_combine_kernel<DT, true, J>), grid, dim3(256), 0, stream, ys, pos, w, y, a.T, a.topk, a.vecs, lg,
+                           a.ldx16);
     else
-        hipLaunchKernelGGL((moe_combine_kernel<DT, false>), dim3(unsigned(blocks)), dim3(256), 0, stream, ys, pos, w, y,
-                           a.T, a.topk, a.vecs, pieces, a.ldx16);
+        hipLaunchKernelGGL((moe_combine_kernel<DT, false, J>), grid, dim3(256), 0, stream, ys, pos, w, y, a.T, a.topk,
+                           a.vecs, lg, a.ldx16);
+    return hipGetLastError();
+}
+
+// choices loaded together: no more than a token has, up to eight
+template <int DT>
+hipError_t combine_dt(const MoeArgs &a, const void *Ys, const int32_t *pos, const float *w, void *Y, hipStream_t stream)
+{
+    return a.topk <= 2   ? combine_j<DT, 2>(a, Ys, pos, w, Y, stream)
+           : a.topk <= 4 ? combine_j<DT, 4>(a, Ys, pos, w, Y, stream)
+                         : combine_j<DT, 8>(a, Ys, pos, w, Y, stream);
+}
+
+template <int DT, int J>
+hipError_t grad_j(const MoeArgs &a, const void *dY, const void *Ys, const int32_t *pos, const float *w, void *dYs,
+                  float *dw, hipStream_t stream)
+{
+    hipLaunchKernelGGL((moe_combine_grad_kernel<DT, J>), dim3(a.T), dim3(256), 0, stream, static_cast<const u32x4 *>(dY),
+                       static_cast<const u32x4 *>(Ys), pos, w, static_cast<u32x4 *>(dYs), dw, a.T, a.topk, a.vecs, a.ldx16);
     return hipGetLastError();
 }
 
@@ -473,9 +542,9 @@ template <int DT>
 hipError_t grad_dt(const MoeArgs &a, const void *dY, const void *Ys, const int32_t *pos, const float *w, void *dYs,
                    float *dw, hipStream_t stream)
 {
-    hipLaunchKernelGGL((moe_combine_grad_kernel<DT>), dim3(a.T), dim3(256), 0, stream, static_cast<const u32x4 *>(dY),
-                       static_cast<const u32x4 *>(Ys), pos, w, static_cast<u32x4 *>(dYs), dw, a.T, a.topk, a.vecs, a.ldx16);
-    return hipGetLastError();
+    return a.topk <= 2   ? grad_j<DT, 2>(a, dY, Ys, pos, w, dYs, dw, stream)
+           : a.topk <= 4 ? grad_j<DT, 4>(a, dY, Ys, pos, w, dYs, dw, stream)
+                         : grad_j<DT, 8>(a, dY, Ys, pos, w, dYs, dw, stream);
 }
 
 }  // namespace
