@@ -47,6 +47,8 @@ EXTRA_FLAGS = {
     "gemm256_bf16_amn_bmn.hip": _MAX_ILP,
     "gemm256_f16_amn_bmn.hip": _MAX_ILP,
     "gemm_skinny_sk.hip": _MAX_ILP,
+    "gemm_grouped_k_bf16.hip": _MAX_ILP,
+    "gemm_grouped_k_f16.hip": _MAX_ILP,
 }
 
 

@@ -27,8 +27,10 @@ grouped_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ B, con
 {
     static_assert(!A_MN || B_MN, "along K both operands are MN-major");
     constexpr bool kMf16 = !A_MN;   // both MN-major: 32x32x16 MFMAs, as in gemm256_kernel
-    __shared__ __attribute__((aligned(1024))) uint8_t lds0[kStage];
-    __shared__ __attribute__((aligned(1024))) uint8_t lds1[kStage];
+    // Two stages of A and three of B, all of the LDS.  A group's B is its own,
+    // so unlike one large product's it is fetched from memory by the one XCD
+    // that works on the group, and memory's latency is longer than a step.
+    __shared__ __attribute__((aligned(1024))) uint8_t a0[kATile], a1[kATile], b0[kBTile], b1[kBTile], b2[kBTile];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -71,19 +73,23 @@ grouped_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ B, con
     else
         da.init(Ag, m0, rows_a, uint32_t(K) * 2, wave, lane, 0);
     if constexpr (B_MN)
-        dmb.init(Bg, N, N, n0, Kg, wave, lane, kATile);
+        dmb.init(Bg, N, N, n0, Kg, wave, lane, 0);
     else
-        db.init(Bg, n0, rows_b, uint32_t(K) * 2, wave, lane, kATile);
-    auto issue = [&](uint8_t *stage, int kt) {
+        db.init(Bg, n0, rows_b, uint32_t(K) * 2, wave, lane, 0);
+    auto issue_a = [&](uint8_t *stage, int kt) {
         if constexpr (A_MN)
             dma.issue(stage, kt);
         else
             da.issue(stage, kt);
+    };
+    auto issue_b = [&](uint8_t *stage, int kt) {
         if constexpr (B_MN)
             dmb.issue(stage, kt);
         else
             db.issue(stage, kt);
     };
+    constexpr int kCopies = DmaOperand<W>::kInstr;   // copy instructions of one operand and step
+    static_assert(kCopies == DmaMnOperand<W>::kInstr, "either layout");
 
     constexpr int TM = kMf16 ? 8 : 4, TN = kMf16 ? 4 : 2;
     using Acc = std::conditional_t<kMf16, f32x4, f32x16>;
@@ -93,9 +99,9 @@ grouped_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ B, con
         abase[i] = kMf16 ? kfrag_base<false>(0, wm, i, kblk16(lane >> 4), lane) : mn_frag_base(0, wm + 32 * i, lane);
 #pragma unroll
     for (int j = 0; j < TN; ++j)
-        bbase[j] = !kMf16  ? mn_frag_base(kATile, wn + 32 * j, lane)
-                   : B_MN ? mn_frag_base16(kATile, wn + 16 * j, lane)
-                          : kfrag_base<false>(kATile, wn, j, kblk16(lane >> 4), lane);
+        bbase[j] = !kMf16  ? mn_frag_base(0, wn + 32 * j, lane)
+                   : B_MN ? mn_frag_base16(0, wn + 16 * j, lane)
+                          : kfrag_base<false>(0, wn, j, kblk16(lane >> 4), lane);
     Acc acc[TN][TM];
 #pragma unroll
     for (int j = 0; j < TN; ++j)
@@ -103,7 +109,7 @@ grouped_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ B, con
         for (int i = 0; i < TM; ++i)
             acc[j][i] = Acc{};
 
-    auto compute = [&](const uint8_t *s) {
+    auto compute = [&](const uint8_t *sa, const uint8_t *sb) {
         uint32_t ab[TM], bb[TN];
 #pragma unroll
         for (int i = 0; i < TM; ++i)
@@ -117,15 +123,15 @@ grouped_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ B, con
                 u32x4 af[TM], bf[TN];
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
-                    af[i] = lds_read16(s, ab[i] ^ uint32_t(ks << 6));
+                    af[i] = lds_read16(sa, ab[i] ^ uint32_t(ks << 6));
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
                     if constexpr (B_MN) {
-                        const u32x2 x = lds_read_tr16(s, bb[j] + uint32_t(32 * ks) * kMnRowBytes);
-                        const u32x2 y = lds_read_tr16(s, bb[j] + uint32_t(32 * ks + 4) * kMnRowBytes);
+                        const u32x2 x = lds_read_tr16(sb, bb[j] + uint32_t(32 * ks) * kMnRowBytes);
+                        const u32x2 y = lds_read_tr16(sb, bb[j] + uint32_t(32 * ks + 4) * kMnRowBytes);
                         bf[j] = u32x4{x[0], x[1], y[0], y[1]};
                     } else {
-                        bf[j] = lds_read16(s, bb[j] ^ uint32_t(ks << 6));
+                        bf[j] = lds_read16(sb, bb[j] ^ uint32_t(ks << 6));
                     }
                 }
 #pragma unroll
@@ -135,7 +141,7 @@ grouped_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ B, con
                         acc[j][i] = mfma_16x16x32<BF16>(bf[j], af[i], acc[j][i]);
             }
         } else {
-            auto frag = [&](uint32_t base, int ks) {
+            auto frag = [&](const uint8_t *s, uint32_t base, int ks) {
                 const uint32_t b = base ^ uint32_t((ks & 1) << 5);
                 const u32x2 x = lds_read_tr16(s, b + uint32_t(16 * ks) * kMnRowBytes);
                 const u32x2 y = lds_read_tr16(s, b + uint32_t(16 * ks + 4) * kMnRowBytes);
@@ -145,10 +151,10 @@ grouped_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ B, con
             auto rd = [&](int ks) {
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
-                    af[ks & 1][i] = frag(ab[i], ks);
+                    af[ks & 1][i] = frag(sa, ab[i], ks);
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
-                    bf[ks & 1][j] = frag(bb[j], ks);
+                    bf[ks & 1][j] = frag(sb, bb[j], ks);
             };
             rd(0);
 #pragma unroll
@@ -164,62 +170,123 @@ grouped_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ B, con
         }
     };
 
-    // two K steps per iteration, one stage each (gemm256_kernel's main loop)
+    // Step t computes from A's stage t % 2 and B's stage t % 3 while A's copies
+    // of step t + 1 and B's of step t + 2 are on their way; the barrier that
+    // ends it leaves B's in flight.  Copies beyond the last step repeat it into
+    // stages that nobody reads again.
     const int KT = Kg / 64;
+    auto stage_a = [&](int u) { return u % 2 == 0 ? a0 : a1; };
+    auto stage_b = [&](int u) { return u % 3 == 0 ? b0 : u % 3 == 1 ? b1 : b2; };
     if (KT > 0) {
-        issue(lds0, 0);
-        __syncthreads();
-        int kt = 0;
-        for (; kt + 1 < KT; kt += 2) {
-            issue(lds1, kt + 1);
-            compute(lds0);
-            lds_barrier_keep_vm<0>();
-            issue(lds0, min(kt + 2, KT - 1));
-            compute(lds1);
-            lds_barrier_keep_vm<0>();
-        }
-        if (kt < KT)
-            compute(lds0);
-        __syncthreads();   // no copy may still be writing LDS when the workgroup ends
+        issue_a(a0, 0);
+        issue_b(b0, 0);
+        issue_b(b1, min(1, KT - 1));
+        lds_barrier_keep_vm<kCopies>();
+        auto step = [&](auto uc, int t) {
+            constexpr int u = decltype(uc)::value;
+            issue_a(stage_a(u + 1), min(t + 1, KT - 1));
+            issue_b(stage_b(u + 2), min(t + 2, KT - 1));
+            compute(stage_a(u), stage_b(u));
+            lds_barrier_keep_vm<kCopies>();
+        };
+        int t = 0;
+        for (; t + 6 <= KT; t += 6)
+            static_for<0, 6>([&](auto uc) { step(uc, t + decltype(uc)::value); });
+        static_for<0, 5>([&](auto uc) {
+            if (t + decltype(uc)::value < KT)
+                step(uc, t + decltype(uc)::value);
+        });
+        lds_barrier_keep_vm<0>();   // no copy may still be writing LDS when the workgroup ends
     }
     if (Kg % 64) {
         // the partial last step: K values beyond the group read as zeros
-        lds_barrier_keep_vm<0>();
         if constexpr (A_MN)
-            dma.issue_tail(lds0, KT, Kg, wave, lane);
+            dma.issue_tail(a0, KT, Kg, wave, lane);
         else
-            da.issue_tail(lds0, KT, uint32_t(Kg % 64) * 2, wave, lane);
+            da.issue_tail(a0, KT, uint32_t(Kg % 64) * 2, wave, lane);
         if constexpr (B_MN)
-            dmb.issue_tail(lds0, KT, Kg, wave, lane);
+            dmb.issue_tail(b0, KT, Kg, wave, lane);
         else
-            db.issue_tail(lds0, KT, uint32_t(Kg % 64) * 2, wave, lane);
+            db.issue_tail(b0, KT, uint32_t(Kg % 64) * 2, wave, lane);
         lds_barrier_keep_vm<0>();
-        compute(lds0);
+        compute(a0, b0);
     }
 
-    // D's rows start at the group's (along M) or at the group's matrix (along K)
+    // D's rows start at the group's (along M) or at the group's matrix (along K).
+    // The tile goes to memory through the (now idle) stages, each wave's part
+    // through 16 KiB of its own, so that stores cover whole 128-byte lines of
+    // D's rows and can pass the caches: the MFMA's layout gives a row 32 or 64
+    // bytes per store.
     const size_t d0 = (A_MN ? size_t(e) * M + m0 : size_t(lo) + m0) * N;
-    if constexpr (kMf16) {
+    __syncthreads();
+    uint8_t *const area = (wave < 2 ? a0 : wave < 4 ? a1 : wave < 6 ? b0 : b1) + (wave & 1) * (kATile / 2);
+    // MFMA block (i, j), register group h: row and 4-column piece in the wave's part
+    constexpr int kPieces = kMf16 ? 1 : 4, kBlockRows = kMf16 ? 16 : 32;
+    const int row0 = lane % kBlockRows, piece0 = kMf16 ? lane >> 4 : lane >> 5;
+    auto values = [&](int i, int j, int h) {
+        return f32x4{acc[j][i][4 * h], acc[j][i][4 * h + 1], acc[j][i][4 * h + 2], acc[j][i][4 * h + 3]};
+    };
+    if constexpr (OUT == kOutF32) {
+        // 32 rows of 256 bytes at a time, 16-byte chunks XOR-keyed by row
+        // (layout.hpp, epi_key)
+        static_for<0, 4>([&](auto qc) {
+            constexpr int qr = decltype(qc)::value, kI = 32 / kBlockRows;
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+            for (int ii = 0; ii < kI; ++ii)
 #pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                const int m = wm + 16 * i + (lane & 15), n = n0 + wn + 16 * j + 4 * (lane >> 4);
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int h = 0; h < kPieces; ++h) {
+                        const uint32_t row = kBlockRows * ii + row0, c = kMf16 ? 4 * j + piece0 : 8 * j + 2 * h + piece0;
+                        *reinterpret_cast<f32x4 *>(area + row * kEpiPitch + ((c ^ epi_key(row)) << 4)) =
+                            values(kI * qr + ii, j, h);
+                    }
+            wave_lds_sync();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const f32x4 v = *reinterpret_cast<const f32x4 *>(area + epi_read_offset(k, lane));
+                const int m = wm + 32 * qr + 4 * k + (lane >> 4), n = n0 + wn + 4 * (lane & 15);
                 if (m < rows_a && n < N)
-                    store_d4<OUT, BETA, OUT == kOutF32>(D, d0 + size_t(m) * N + n, acc[j][i]);
+                    store_d4<OUT, BETA, true>(D, d0 + size_t(m) * N + n, v);
             }
+            wave_lds_sync();   // the next quarter's writes come after these reads
+        });
+    } else if constexpr (!BETA) {
+        // all 128 rows of 128 bytes, 16-byte chunk c of row m at c ^ (m % 8)
+        using T = std::conditional_t<OUT == kOutBf16, __bf16, _Float16>;
+        typedef T t4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int h = 0; h < kPieces; ++h) {
+                    const f32x4 v = values(i, j, h);
+                    const t4 t = {T(v[0]), T(v[1]), T(v[2]), T(v[3])};
+                    const uint32_t row = kBlockRows * i + row0, p = kMf16 ? 4 * j + piece0 : 8 * j + 2 * h + piece0;
+                    *reinterpret_cast<t4 *>(area + row * 128 + (((p >> 1) ^ (row & 7)) << 4) + 8 * (p & 1)) = t;
+                }
+        wave_lds_sync();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const uint32_t row = 8 * k + (lane >> 3), c = lane & 7;
+            const u32x4 v = lds_read16(area, row * 128 + ((c ^ (row & 7)) << 4));
+            const int m = wm + int(row), n = n0 + wn + 8 * int(c);
+            if (m < rows_a && n < N)
+                __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(static_cast<T *>(D) + d0 + size_t(m) * N + n));
+        }
     } else {
+        // D's old value is added before the one rounding
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+            for (int j = 0; j < TN; ++j)
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const int m = wm + 32 * i + (lane & 31), n = n0 + wn + 32 * j + 8 * h + 4 * (lane >> 5);
+                for (int h = 0; h < kPieces; ++h) {
+                    const int m = wm + kBlockRows * i + row0;
+                    const int n = n0 + wn + 4 * (kMf16 ? 4 * j + piece0 : 8 * j + 2 * h + piece0);
                     if (m < rows_a && n < N)
-                        store_d4<OUT, BETA>(D, d0 + size_t(m) * N + n,
-                                            f32x4{acc[j][i][4 * h], acc[j][i][4 * h + 1], acc[j][i][4 * h + 2],
-                                                  acc[j][i][4 * h + 3]});
+                        store_d4<OUT, true>(D, d0 + size_t(m) * N + n, values(i, j, h));
                 }
     }
 }
