@@ -126,6 +126,25 @@ __device__ __forceinline__ bool group_of_tile(const int32_t *offsets, int E, int
     return false;
 }
 
+// The group that comes at place `rank` when groups are ordered by length, the
+// longest first (equal ones in their own order); up to 64 groups, more keep
+// their own order.  Every lane takes part.
+__device__ __forceinline__ int group_by_length(const int32_t *offsets, int E, int rows, int rank, int lane)
+{
+    if (E > 64)
+        return rank;
+    int lo = 0, hi = -1;
+    if (lane < E)
+        group_bounds(offsets, lane, rows, lo, hi);
+    const int mine = hi - lo;
+    int before = 0;
+    for (int i = 0; i < E; ++i) {
+        const int other = __builtin_amdgcn_readlane(mine, i);
+        before += other > mine || (other == mine && i < lane);
+    }
+    return __builtin_ctzll(__ballot(lane < E && before == rank));
+}
+
 // Most row tiles that E groups of together at most `rows` rows can make.
 inline int64_t most_tiles(int64_t E, int64_t rows, int64_t tile_rows)
 {

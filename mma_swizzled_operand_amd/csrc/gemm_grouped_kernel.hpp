@@ -19,6 +19,7 @@ namespace mswz {
 namespace {
 
 constexpr int kRaster = 4;   // row tiles whose column tiles are walked together
+constexpr int kCusPerXcd = 32;
 
 template <bool BF16, bool A_MN, bool B_MN, int OUT, bool BETA>
 __global__ void __launch_bounds__(64 * W)
@@ -34,35 +35,52 @@ grouped_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ B, con
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // workgroup -> tile: each XCD (workgroup number % 8) takes one contiguous
-    // run of the tiles that exist
-    int e = 0, tm = 0, tn = 0, lo = 0, hi = 0;
-    const int mt = A_MN ? E * tiles_m : group_tiles(offsets, E, M, kBM, lane);
-    const int total = mt * tiles_n, per = (total + 7) / 8;
-    const int id = int(blockIdx.x & 7u) * per + int(blockIdx.x >> 3);
-    if (int(blockIdx.x >> 3) >= per || id >= total)
-        return;
-    {
-        const int span = kRaster * tiles_n, first = id / span * kRaster, in = id % span;
-        const int rows = min(kRaster, mt - first);
-        tm = first + in % rows;
-        tn = in / rows;
-    }
+    int e = 0, tm = 0, tn = 0, lo = 0, hi = 0, height = kBM;
+    bool second = false;   // the lower half of a tile that two workgroups share
     if constexpr (A_MN) {
-        e = tm / tiles_m;
-        tm -= e * tiles_m;
+        // Every group has the same tiles; the longest groups go first, and each
+        // is spread over all XCDs, so that the workgroups that start last are
+        // the short ones.
+        const int tiles = tiles_m * tiles_n, rank = int(blockIdx.x) / tiles;
+        if (rank >= E)
+            return;
+        e = group_by_length(offsets, E, K, rank, lane);
+        tile_of_block(int(blockIdx.x) - rank * tiles, tiles_m, tiles_n, -kRaster, tm, tn);
         group_bounds(offsets, e, K, lo, hi);
     } else {
+        // Each XCD (workgroup number % 8) takes one contiguous run of the row
+        // tiles x column tiles that exist.  Its last round of 32 workgroups, if
+        // at most half full, is cut into tiles of half the rows.
+        const int mt = group_tiles(offsets, E, M, kBM, lane), total = mt * tiles_n, per = (total + 7) / 8;
+        const int xcd = int(blockIdx.x & 7u), at = int(blockIdx.x >> 3);
+        const int left = per % kCusPerXcd, halves = left <= kCusPerXcd / 2 ? left : 0;
+        int id = at;
+        if (at >= per - halves) {
+            id = per - halves + (at - (per - halves)) / 2;
+            height = kBM / 2;
+            second = (at - (per - halves)) % 2;
+        }
+        if (id >= per || xcd * per + id >= total)
+            return;
+        id += xcd * per;
+        const int span = kRaster * tiles_n, first = id / span * kRaster, in = id % span;
+        const int rows = min(kRaster, mt - first);
         int t;
-        group_of_tile(offsets, E, M, kBM, tm, lane, e, t, lo, hi);
+        group_of_tile(offsets, E, M, kBM, first + in % rows, lane, e, t, lo, hi);
         tm = t;
+        tn = in / rows;
     }
     const int Kg = A_MN ? hi - lo : K;          // K values of this tile
     const int Mg = A_MN ? M : hi - lo;          // rows of this tile's matrix
-    const int m0 = tm * kBM, n0 = tn * kBN;
-    const int rows_a = min(kBM, Mg - m0), rows_b = min(kBN, N - n0);
+    const int m0 = tm * kBM + (second ? kBM / 2 : 0), n0 = tn * kBN;
+    const int rows_a = min(height, Mg - m0), rows_b = min(kBN, N - n0);
+    if (rows_a <= 0)
+        return;
     constexpr int kWavesN = 4;
     const int wm = (wave / kWavesN) * 128, wn = (wave % kWavesN) * 64;
+    // a wave whose part lies outside D copies and waits with the others, and
+    // leaves the matrix units to the wave that shares its SIMD
+    const bool idle = wm >= rows_a || n0 + wn >= N;
 
     const uint8_t *Ag = A + (A_MN ? size_t(lo) * M : size_t(lo) * K) * 2;
     const uint8_t *Bg = B + (A_MN ? size_t(lo) * N : size_t(e) * N * K) * 2;
@@ -186,7 +204,8 @@ grouped_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ B, con
             constexpr int u = decltype(uc)::value;
             issue_a(stage_a(u + 1), min(t + 1, KT - 1));
             issue_b(stage_b(u + 2), min(t + 2, KT - 1));
-            compute(stage_a(u), stage_b(u));
+            if (!idle)
+                compute(stage_a(u), stage_b(u));
             lds_barrier_keep_vm<kCopies>();
         };
         int t = 0;
@@ -297,7 +316,8 @@ hipError_t launch_grouped_out(const GroupedArgs &a, hipStream_t stream)
     const int64_t tiles_m = A_MN ? (a.M + kBM - 1) / kBM : most_tiles(a.E, a.M, kBM);
     const int64_t tiles_n = (a.N + kBN - 1) / kBN;
     const int64_t tiles = tiles_m * tiles_n * (A_MN ? a.E : 1);
-    const dim3 grid(unsigned((tiles + 7) / 8 * 8));   // each XCD the same number
+    // along M each XCD the same number, and room for its halved last round
+    const dim3 grid(unsigned(A_MN ? tiles : ((tiles + 7) / 8 + kCusPerXcd / 2) * 8));
     const uint8_t *A = static_cast<const uint8_t *>(a.A), *B = static_cast<const uint8_t *>(a.B);
     if (a.beta)
         hipLaunchKernelGGL((grouped_kernel<BF16, A_MN, B_MN, OUT, true>), grid, dim3(64 * W), 0, stream, A, B, a.offsets,
