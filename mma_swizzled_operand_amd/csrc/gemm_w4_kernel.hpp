@@ -44,7 +44,16 @@ namespace {
 
 constexpr int kW4Threads = 512;
 constexpr int kChunk = 128;               // K values of one 16-byte load of all four lane groups
-constexpr int kStages = 4, kAhead = 3;    // LDS stages of A and register slots; steps in flight
+
+// Compile-time loop: fn(std::integral_constant<int, F>), ..., up to L - 1.
+template <int F, int L, class Fn>
+__device__ __forceinline__ void static_for(Fn &&fn)
+{
+    if constexpr (F < L) {
+        fn(std::integral_constant<int, F>{});
+        static_for<F + 1, L>(fn);
+    }
+}
 
 // Eight 4-bit integers of a dword as 16-bit floats, in element order.  A byte
 // 0..15 read as E4M3 is that many times 2^-9 (subnormal up to 7, the first
@@ -174,7 +183,7 @@ struct W4Kernel {
     int part_steps;       // steps of one part of K
 };
 
-template <bool BF16, bool E2M1, int SPAN, int ROWS, int NB, int NG, int OUT, bool SPLIT>
+template <bool BF16, bool E2M1, int SPAN, int ROWS, int NB, int NG, int STAGES, int OUT, bool SPLIT>
 __global__ void __launch_bounds__(kW4Threads)
 w4_kernel(W4Kernel p)
 {
@@ -185,9 +194,9 @@ w4_kernel(W4Kernel p)
     constexpr int kSpans = 128 / SPAN, kPer = 4 / kSpans;   // scale groups of a chunk, MFMAs of one
     constexpr int kCols = 16 * NB * NG;
     // A's part of a stage, in whole copies by all waves (what lies behind the
-    // rows is written as zeros and not read)
-    constexpr int kCopies = (ROWS * KQ * 16 + kW4Threads - 1) / kW4Threads, kABytes = kCopies * kW4Threads * 16;
-    static_assert(4 * NB * MB * 1024 <= kABytes, "the waves' sums fit into two stages");
+    // rows is written as zeros and not read); two of them take the waves' sums
+    constexpr int kCopies = (ROWS * KQ * 16 + kW4Threads - 1) / kW4Threads;
+    constexpr int kABytes = kCopies * kW4Threads * 16 > 4 * NB * MB * 1024 ? kCopies * kW4Threads * 16 : 4 * NB * MB * 1024;
     // A step's scales of one column lie next to each other in memory, at any
     // byte; they are copied as the aligned words that hold them.  Scales are
     // copied by waves 0-3 and zero points by 4-7 (FP4: scales by all).
@@ -200,8 +209,15 @@ w4_kernel(W4Kernel p)
     constexpr int kStageBytes = kABytes + (E2M1 ? 1 : 2) * kSBytes;
     // one named array per stage: the compiler then knows which stage a copy
     // writes, and waits for no other one
-    __shared__ __attribute__((aligned(1024))) uint8_t st0[kStageBytes], st1[kStageBytes], st2[kStageBytes], st3[kStageBytes];
-    auto stage = [&](int u) { return u == 0 ? st0 : u == 1 ? st1 : u == 2 ? st2 : st3; };
+    constexpr int kStages = STAGES, kAhead = STAGES - 1;   // LDS stages and register slots; steps in flight
+    static_assert(STAGES >= 2 && STAGES <= 8, "named stages");
+#define W4_STAGE(i) \
+    __shared__ __attribute__((aligned(1024))) uint8_t st##i[i < STAGES ? kStageBytes : 4];
+    W4_STAGE(0) W4_STAGE(1) W4_STAGE(2) W4_STAGE(3) W4_STAGE(4) W4_STAGE(5) W4_STAGE(6) W4_STAGE(7)
+#undef W4_STAGE
+    auto stage = [&](int u) {
+        return u == 0 ? st0 : u == 1 ? st1 : u == 2 ? st2 : u == 3 ? st3 : u == 4 ? st4 : u == 5 ? st5 : u == 6 ? st6 : st7;
+    };
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, q = lane >> 4, ng = wave % NG, kq = wave / NG;
@@ -214,10 +230,11 @@ w4_kernel(W4Kernel p)
     const int first = SPLIT ? int(blockIdx.z) * p.part_steps : 0;
     const int steps = SPLIT ? min(p.part_steps, all_steps - first) : all_steps;
 
-    // ---- per-lane offsets of the loads.  Rows beyond N or the tile, and K values
-    // beyond K, point at the ends of the buffers' ranges and read as zeros; by
-    // selects, since with a branch for the last step a register might be the
-    // target of either side's load and every load in flight was waited for.
+    // ---- per-lane offsets of the loads.  Rows beyond N or the tile, and A's
+    // values beyond K, lie outside the buffers' ranges and read as zeros (the
+    // latter by selects: with a branch for the last step a register might be the
+    // target of either side's load, and every load in flight was waited for).
+    // Weights beyond K, the next row's or zeros, meet those zeros.
     const uint32_t row_bytes = uint32_t(p.K) / 2;
     const uint32_t w_bytes = uint32_t(p.N) * row_bytes;
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.B + size_t(e) * w_bytes, w_bytes);
@@ -245,7 +262,7 @@ w4_kernel(W4Kernel p)
         const uint32_t u = uint32_t(tid % kSThreads + kSThreads * i), words = zeros ? kZWords : kSWords;
         const uint32_t col = u / words, n = n0 + col;
         s_word[i] = 4 * (u - col * words);
-        s_off[i] = col < kCols && n < uint32_t(p.N) ? (zeros ? z_skip : s_skip) + n * uint32_t(p.groups) * (zeros ? 1 : kSize) : ~0u;
+        s_off[i] = col < kCols && n < uint32_t(p.N) ? (zeros ? z_skip : s_skip) + n * uint32_t(p.groups) * (zeros ? 1 : kSize) : 0x80000000u;   // (beyond any range, with any scale's offset)
     }
     auto group_of = [&](int c) {   // first scale of chunk c
         return kPre ? 4 * c : SPAN < 128 ? kSpans * c : int((uint64_t(c) * p.group_magic) >> 32);
@@ -262,7 +279,7 @@ w4_kernel(W4Kernel p)
 
     u32x4 w[kStages][NB];
     // all loads of step t (a step beyond the last repeats it: never used)
-    auto load = [&](int slot, uint8_t *st, int t) {
+    auto load = [&](int slot, uint8_t *st, int t) __attribute__((always_inline)) {
         const int c0 = (first + min(t, steps - 1)) * KQ;          // first chunk of the step
         const uint32_t kb = uint32_t(c0) * 64;
         const int left = p.K - c0 * kChunk;     // K values from the step's first on
@@ -273,10 +290,10 @@ w4_kernel(W4Kernel p)
 #pragma unroll
         for (int i = 0; i < kSCopies; ++i)
             buffer_load_lds4(rs, st + kABytes + (zeros ? kSBytes : 0) + 4 * (kSThreads * i + 64 * (wave % (kSThreads / 64))),
-                             s_off[i] == ~0u ? s_bytes : ((s_off[i] + g0) & ~3u) + s_word[i], 0);
+                             ((s_off[i] + g0) & ~3u) + s_word[i], 0);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
-            w[slot][nb] = buffer_load16(rw, kChunk * kq + 32 * q < left ? w_off[nb] + kb : w_bytes, 0);
+            w[slot][nb] = buffer_load16(rw, w_off[nb] + kb, 0);
     };
     constexpr int kLoads = kCopies + kSCopies + NB;   // vector-memory operations of one step
 
@@ -288,24 +305,62 @@ w4_kernel(W4Kernel p)
             acc[nb][mb] = f32x4{};
     const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 
-    // A's fragments: piece c of row r of block mb
-    auto piece = [&](const uint8_t *st, int mb, int j) {
-        const int m = (16 * mb + r) % ROWS;
-        return lds_read16(st, 16 * uint32_t((m * KQ + kq) * 16 + (w4_piece<SPAN>(j, q) ^ row_key<SPAN>(m))));
+    // A's fragments: the lane's piece of row r for MFMA j and row block mb, i.e.
+    // one base, XOR a constant of j, plus one of mb (opaque: else every sum of
+    // them is kept in a register of its own through the loop)
+    const uint32_t a_base = 16u * uint32_t((r % ROWS * KQ + kq) * 16 + (w4_piece<SPAN>(0, q) ^ row_key<SPAN>(r % ROWS)));
+    auto pieces = [&](const uint8_t *st, int j, u32x4 *av) __attribute__((always_inline)) {
+        const uint32_t at = opaque(a_base ^ uint32_t(16 * w4_piece<SPAN>(j, 0)));
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+            av[mb] = lds_read16(st, at + uint32_t(mb * 16 * KQ * 256));
     };
-    // scale (zero point) g of the chunk for this lane's column of block nb; t is
-    // the step that the stage holds.  A whole chunk without scales (behind K)
-    // has no value of A either, but a scale that is not finite would still count.
-    auto scale_of = [&](const uint8_t *st, int t, int nb, int g, bool z) {
-        const int c0 = (first + t) * KQ, gi = group_of(c0 + kq) + g, col = 16 * (NB * ng + nb) + r;
-        const uint32_t size = z ? 1 : kSize, skip = z ? z_skip : s_skip;
-        const uint32_t at = skip + (uint32_t(n0 + col) * uint32_t(p.groups) + uint32_t(group_of(c0))) * size;
-        const uint8_t *b = st + kABytes + (z ? kSBytes : 0) + 4 * (z ? kZWords : kSWords) * col + (at & 3) +
-                           (gi - group_of(c0)) * size;
-        const uint32_t v = size == 2 ? *reinterpret_cast<const uint16_t *>(b) : *b;
-        return gi < p.groups ? v : 0u;
+    // This lane's scales and zero points (absent ones are copied as zeros) of
+    // column block nb, step t in the stage: spans 0 .. kSpans - 1 of the wave's
+    // chunk (folded scales: the lane group's own).  A scale behind the last one
+    // has no value of A either, but if it was not finite it would still count.
+    const uint32_t no_z = p.Z ? 0u : 8u;
+    const uint32_t s_col = uint32_t(n0 + 16 * NB * ng + r) * uint32_t(p.groups);   // first scale of block 0's column
+    // bytes of block nb's first scale and zero point past a word, and their words' places
+    uint32_t s_mod[NB], z_mod[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        s_mod[nb] = s_skip + (s_col + uint32_t(16 * nb * p.groups)) * kSize;
+        z_mod[nb] = z_skip + s_col + uint32_t(16 * nb * p.groups);
+    }
+    const uint32_t s_place = uint32_t(kABytes + 4 * kSWords * (16 * NB * ng + r) + (kPre ? q : 0));
+    const uint32_t z_place = uint32_t(kABytes + kSBytes + 4 * kZWords * (16 * NB * ng + r));
+    auto scales = [&](const uint8_t *st, int t, int nb, uint32_t *sv, uint32_t *zv) __attribute__((always_inline)) {
+        const int c0 = (first + t) * KQ, g0 = group_of(c0), g1 = group_of(c0 + kq);
+        const uint32_t s_at = ((s_mod[nb] + uint32_t(g0) * kSize) & 3) + (s_place + uint32_t(g1 - g0) * kSize);
+#pragma unroll
+        for (int g = 0; g < kSpans; ++g) {
+            const uint8_t *b = st + s_at + 64 * kSWords * nb + kSize * g;
+            sv[g] = kSize == 2 ? *reinterpret_cast<const uint16_t *>(b) : *b;
+        }
+        if constexpr (!E2M1) {
+            const uint32_t z_at = ((z_mod[nb] + uint32_t(g0)) & 3) + (z_place + uint32_t(g1 - g0));
+#pragma unroll
+            for (int g = 0; g < kSpans; ++g)
+                zv[g] = *(st + z_at + 64 * kZWords * nb + g);
+        }
+#pragma unroll
+        for (int g = 0; g < kSpans; ++g)   // (no branch: it would cost the loop its registers)
+            sv[g] &= uint32_t((g1 + (kPre ? q : g) - p.groups) >> 31);
     };
-    auto compute = [&](const uint8_t *st, int slot, int t) {
+    // A step's LDS reads all come before the work on them (64 rows: one MFMA's
+    // rows ahead), since two waves a SIMD cannot hide one read's latency after
+    // the other.
+    constexpr int kReads = MB > 1 ? 2 : 4;
+    auto compute = [&](const uint8_t *st, int slot, int t) __attribute__((always_inline)) {
+        uint32_t sv[NB][kSpans], zv[NB][kSpans];
+        u32x4 av[kReads][MB];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+            scales(st, t, nb, sv[nb], zv[nb]);
+#pragma unroll
+        for (int j = 0; j < kReads; ++j)
+            pieces(st, j, av[j]);
         if constexpr (kPre) {
             float scale[NB];
 #pragma unroll
@@ -313,45 +368,44 @@ w4_kernel(W4Kernel p)
                 // 2^(ex - 127), ex = 255 converting to NaN.  Weights above 2 times
                 // the largest two would pass bf16's range: those blocks are
                 // multiplied unscaled, one lane group at a time, and their sums
-                // scaled afterwards.
-                const uint32_t ex = scale_of(st, t, nb, q, false);
+                // scaled afterwards (what they add here, 2^-253 of that, is lost
+                // in the rounding).
+                const uint32_t ex = sv[nb][0];
                 const bool big = ex == 253 || ex == 254;
-                scale[nb] = __builtin_bit_cast(float, ex << 23);
+                scale[nb] = __builtin_bit_cast(float, big ? 0 : ex << 23);
                 if (__any(big)) {
                     for (int g = 0; g < 4; ++g) {
                         const uint32_t exg = __shfl(ex, 16 * g + r);
                         const bool bigg = exg == 253 || exg == 254;
+                        f32x4 part[MB];
 #pragma unroll
-                        for (int mb = 0; mb < MB; ++mb) {
-                            f32x4 part = {};
+                        for (int j = 0; j < 4; ++j) {
+                            const u32x4 v = e2m1_values<BF16>(big && q == g ? w[slot][nb][j] : 0, 1.0f);
+                            u32x4 x[MB];
+                            pieces(st, j, x);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const u32x4 v = e2m1_values<BF16>(big && q == g ? w[slot][nb][j] : 0, 1.0f);
-                                part = mfma_16x16x32<BF16>(piece(st, mb, j), v, part);
-                            }
+                            for (int mb = 0; mb < MB; ++mb)
+                                part[mb] = mfma_16x16x32<BF16>(x[mb], v, j ? part[mb] : f32x4{});
+                        }
+#pragma unroll
+                        for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                acc[nb][mb][i] += bigg ? e8m0_value(exg) * part[i] : 0.0f;
-                        }
+                                acc[nb][mb][i] += bigg ? e8m0_value(exg) * part[mb][i] : 0.0f;
                     }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        w[slot][nb][j] = big ? 0 : w[slot][nb][j];
                 }
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                u32x4 av[MB];
-#pragma unroll
-                for (int mb = 0; mb < MB; ++mb)
-                    av[mb] = piece(st, mb, j);
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                     const u32x4 v = e2m1_values<BF16>(w[slot][nb][j], scale[nb]);
 #pragma unroll
                     for (int mb = 0; mb < MB; ++mb)
-                        acc[nb][mb] = mfma_16x16x32<BF16>(av[mb], v, acc[nb][mb]);
+                        acc[nb][mb] = mfma_16x16x32<BF16>(av[j % kReads][mb], v, acc[nb][mb]);
                 }
+                if (j + kReads < 4)
+                    pieces(st, j + kReads, av[j % kReads]);
             }
             return;
         }
@@ -365,39 +419,40 @@ w4_kernel(W4Kernel p)
             float scale[NB], zero[NB];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-                const uint32_t b = scale_of(st, t, nb, s, false);
                 if constexpr (E2M1) {
-                    scale[nb] = e8m0_value(b);
+                    scale[nb] = e8m0_value(sv[nb][s]);
                 } else {
-                    scale[nb] = scale16<BF16>(uint16_t(b));
-                    zero[nb] = p.Z ? float(scale_of(st, t, nb, s, true)) : 8.0f;
+                    scale[nb] = scale16<BF16>(uint16_t(sv[nb][s]));
+                    zero[nb] = float(zv[nb][s] | no_z);
                     zz[nb] = 0;
                     if constexpr (!BF16)
                         zz[nb] = __builtin_bit_cast(uint16_t, _Float16(zero[nb])) * 0x10001u;
                 }
             }
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                u32x4 av[MB];
-#pragma unroll
-                for (int mb = 0; mb < MB; ++mb) {
-                    av[mb] = piece(st, mb, kPer * s + j);
-                    // the rows' sums over the span, the same in every column
-                    if constexpr (kSums)
-                        sum[mb] = mfma_16x16x32<BF16>(av[mb], ones, j ? sum[mb] : f32x4{});
-                }
+            for (int jj = 0; jj < kPer; ++jj) {
+                const int j = kPer * s + jj;
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
-                    const uint32_t d = w[slot][nb][kPer * s + j];
                     u32x4 v;
                     if constexpr (E2M1)
-                        v = e2m1_values<BF16>(d, 1.0f);
+                        v = e2m1_values<BF16>(w[slot][nb][j], 1.0f);
                     else
-                        v = u4_values<BF16>(d, zz[nb]);
+                        v = u4_values<BF16>(w[slot][nb][j], zz[nb]);
 #pragma unroll
                     for (int mb = 0; mb < MB; ++mb)
-                        part[nb][mb] = mfma_16x16x32<BF16>(av[mb], v, j ? part[nb][mb] : f32x4{});
+                        part[nb][mb] = mfma_16x16x32<BF16>(av[j % kReads][mb], v, jj ? part[nb][mb] : f32x4{});
                 }
+                // the rows' sums over the span, the same in every column
+                if constexpr (kSums)
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb)
+                        sum[mb] = mfma_16x16x32<BF16>(av[j % kReads][mb], ones, jj ? sum[mb] : f32x4{});
+                if (j + kReads < 4)
+                    pieces(st, j + kReads, av[j % kReads]);
+                // (one MFMA row's conversions at a time: all of them spill)
+                if constexpr (MB > 1)
+                    __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
@@ -419,19 +474,32 @@ w4_kernel(W4Kernel p)
         load(u, stage(u), u);
         sched_fence();
     }
-    for (int t0 = 0; t0 < steps; t0 += kStages) {
+    // (Whole rounds of stages without a branch, then the rest: with an exit in
+    // every step the loop's registers had to be copied on the way round, which
+    // waited for all loads in flight.)
+    auto step = [&](auto uc, int t) __attribute__((always_inline)) {
+        constexpr int u = decltype(uc)::value;
+        lds_barrier_keep_vm<(kAhead - 1) * kLoads>();
+        sched_fence();
+        load((u + kAhead) % kStages, stage((u + kAhead) % kStages), t + kAhead);
+        sched_fence();
+        compute(stage(u), u, t);
+        // (the sums are finished here: left open, several steps' products were
+        // kept in registers until the last one's scales came)
 #pragma unroll
-        for (int u = 0; u < kStages; ++u) {
-            if (t0 + u >= steps)
-                break;
-            lds_barrier_keep_vm<(kAhead - 1) * kLoads>();
-            sched_fence();
-            load((u + kAhead) % kStages, stage((u + kAhead) % kStages), t0 + u + kAhead);
-            sched_fence();
-            compute(stage(u), u, t0 + u);
-            sched_fence();
-        }
-    }
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+                acc[nb][mb] = opaque(acc[nb][mb]);
+        sched_fence();
+    };
+    int t = 0;
+    for (; t + kStages <= steps; t += kStages)
+        static_for<0, kStages>([&](auto uc) __attribute__((always_inline)) { step(uc, t + decltype(uc)::value); });
+    static_for<0, kStages - 1>([&](auto uc) __attribute__((always_inline)) {
+        if (t + decltype(uc)::value < steps)
+            step(uc, t + decltype(uc)::value);
+    });
     lds_barrier_keep_vm<0>();   // no copy may still be writing LDS below, or when the workgroup ends
 
     // sums over the KQ waves of a column block: tile tl of column block ng is
@@ -471,7 +539,7 @@ w4_kernel(W4Kernel p)
     }
 }
 
-template <bool BF16, bool E2M1, int SPAN, int ROWS, int NB, int NG, bool SPLIT = false>
+template <bool BF16, bool E2M1, int SPAN, int ROWS, int NB, int NG, int STAGES, bool SPLIT = false>
 hipError_t launch_w4_tile(const W4Args &a, hipStream_t stream)
 {
     constexpr int KQ = 8 / NG, kCols = 16 * NB * NG;
@@ -483,39 +551,44 @@ hipError_t launch_w4_tile(const W4Args &a, hipStream_t stream)
     const dim3 grid((a.N + kCols - 1) / kCols, unsigned(tiles), SPLIT ? (steps + part_steps - 1) / part_steps : 1);
     constexpr int kNarrow = BF16 ? kOutBf16 : kOutF16;
     if constexpr (SPLIT) {
-        hipLaunchKernelGGL((w4_kernel<BF16, E2M1, SPAN, ROWS, NB, NG, kOutF32, true>), grid, dim3(kW4Threads), 0, stream, p);
+        hipLaunchKernelGGL((w4_kernel<BF16, E2M1, SPAN, ROWS, NB, NG, STAGES, kOutF32, true>), grid, dim3(kW4Threads), 0, stream, p);
     } else if (a.out == kOutF32) {
-        hipLaunchKernelGGL((w4_kernel<BF16, E2M1, SPAN, ROWS, NB, NG, kOutF32, false>), grid, dim3(kW4Threads), 0, stream, p);
+        hipLaunchKernelGGL((w4_kernel<BF16, E2M1, SPAN, ROWS, NB, NG, STAGES, kOutF32, false>), grid, dim3(kW4Threads), 0, stream, p);
     } else {
-        hipLaunchKernelGGL((w4_kernel<BF16, E2M1, SPAN, ROWS, NB, NG, kNarrow, false>), grid, dim3(kW4Threads), 0, stream, p);
+        hipLaunchKernelGGL((w4_kernel<BF16, E2M1, SPAN, ROWS, NB, NG, STAGES, kNarrow, false>), grid, dim3(kW4Threads), 0, stream, p);
     }
     return hipGetLastError();
 }
 
 #ifndef W4_TUNE
+// Columns of a workgroup: as many as leave a workgroup for every compute unit
+// (two, for the longest), since more columns share a copy of A and a step's
+// addresses, and make a wave's part of K and with it its run of steps longer.
+// One row by 16384 x 8192, u4: 64 columns 15.9 us, 32 in two blocks of a wave
+// 18.5, 32 in two waves 16.9, 128 (half the units) 37; by 4096 x 4096: 16
+// columns 4.3 us, 32 6.2.
+template <bool BF16, bool E2M1, int SPAN, int ROWS>
+hipError_t launch_w4_cols(const W4Args &a, hipStream_t stream)
+{
+    const int64_t tiles = a.E ? (a.E < a.M ? a.E : a.M) : 1;
+    auto enough = [&](int cols, int wgs) { return tiles * ((a.N + cols - 1) / cols) >= wgs; };
+    // (with 128 columns a stage has room for 16 rows as it is; 16 rows by 16
+    // columns fill a compute unit's LDS, so more than one such workgroup each
+    // would be a second round)
+    return enough(128, 512)                      ? launch_w4_tile<BF16, E2M1, SPAN, 16, 2, 4, 4>(a, stream)
+           : enough(64, 256)                     ? launch_w4_tile<BF16, E2M1, SPAN, ROWS, 2, 2, 4>(a, stream)
+           : enough(32, ROWS == 16 ? 129 : 256) ? launch_w4_tile<BF16, E2M1, SPAN, ROWS, 1, 2, 4>(a, stream)
+                                                 : launch_w4_tile<BF16, E2M1, SPAN, ROWS, 1, 1, 4>(a, stream);
+}
+
 template <bool BF16, bool E2M1, int SPAN>
 hipError_t launch_w4_span(const W4Args &a, hipStream_t stream)
 {
-    // Columns of a workgroup: as many as leave enough workgroups, since more
-    // columns share a copy of A and make a wave's part of K, and with it its
-    // run of steps, longer (16 rows by 16384 x 8192: 18.5 us with 64 columns,
-    // 24.6 with 32; one row by 4096 x 4096: 6.7 us with 32, 4.8 with 16)
-    const int64_t tiles = a.E ? (a.E < a.M ? a.E : a.M) : 1;
-    auto enough = [&](int cols, int wgs) { return tiles * ((a.N + cols - 1) / cols) >= wgs; };
-    switch (w4_rows(a)) {
-    case 4:
-        return enough(128, 512)  ? launch_w4_tile<BF16, E2M1, SPAN, 4, 2, 4>(a, stream)
-               : enough(32, 256) ? launch_w4_tile<BF16, E2M1, SPAN, 4, 2, 1>(a, stream)
-                                 : launch_w4_tile<BF16, E2M1, SPAN, 4, 1, 1>(a, stream);
-    case 16:
-        return enough(128, 512)  ? launch_w4_tile<BF16, E2M1, SPAN, 16, 2, 4>(a, stream)
-               : enough(64, 256) ? launch_w4_tile<BF16, E2M1, SPAN, 16, 2, 2>(a, stream)
-               : enough(32, 256) ? launch_w4_tile<BF16, E2M1, SPAN, 16, 1, 2>(a, stream)
-                                 : launch_w4_tile<BF16, E2M1, SPAN, 16, 1, 1>(a, stream);
-    default:
-        return a.parts > 1 ? launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 4, true>(a, stream)
-                           : launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 4>(a, stream);
-    }
+    const int rows = w4_rows(a);
+    if (rows == 64)
+        return a.parts > 1 ? launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 4, 4, true>(a, stream)
+                           : launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 4, 4>(a, stream);
+    return rows == 16 ? launch_w4_cols<BF16, E2M1, SPAN, 16>(a, stream) : launch_w4_cols<BF16, E2M1, SPAN, 4>(a, stream);
 }
 #endif
 
