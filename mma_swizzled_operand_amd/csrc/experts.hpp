@@ -40,7 +40,8 @@ struct W4Args {
     int parts = 1;           // K parts of the split form (set by launch_w4)
 };
 
-int w4_rows(const W4Args &a);     // rows of the tile that the launch takes
+int w4_rows(const W4Args &a);         // rows of the tile that the launch takes
+int64_t w4_tiles64(const W4Args &a);  // tiles of 64 rows that hold some
 int64_t w4_workspace_bytes(const W4Args &a);
 hipError_t launch_w4(const W4Args &a, hipStream_t stream);
 // one unit per activation and weight kind

@@ -13,20 +13,27 @@
 namespace mswz {
 namespace {
 
-// D = beta*D + the parts' fp32 sums, in part order; one row piece of 256 columns per workgroup.
+// D = beta*D + the parts' fp32 sums, in part order; 1024 columns of a row per
+// workgroup, a thread's four columns loaded together.
 template <int OUT>
 __global__ void __launch_bounds__(256)
 w4_reduce_kernel(const float *__restrict__ ws, void *__restrict__ D, int M, int N, int ldd, int parts, int beta)
 {
-    const int n = blockIdx.x * 256 + threadIdx.x, m = blockIdx.y;
-    if (n >= N)
-        return;
     using T = std::conditional_t<OUT == kOutF32, float, std::conditional_t<OUT == kOutBf16, __bf16, _Float16>>;
-    T *d = static_cast<T *>(D) + size_t(m) * ldd + n;
-    float sum = beta ? float(*d) : 0.0f;
+    const int n0 = blockIdx.x * 1024 + threadIdx.x, m = blockIdx.y;
+    T *const d = static_cast<T *>(D) + size_t(m) * ldd;
+    float sum[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        sum[c] = beta ? float(d[min(n0 + 256 * c, N - 1)]) : 0.0f;
     for (int i = 0; i < parts; ++i)
-        sum += ws[(size_t(i) * M + m) * N + n];
-    *d = T(sum);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            sum[c] += ws[(size_t(i) * M + m) * N + min(n0 + 256 * c, N - 1)];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        if (n0 + 256 * c < N)
+            d[n0 + 256 * c] = T(sum[c]);
 }
 
 }  // namespace
@@ -38,14 +45,16 @@ int w4_rows(const W4Args &a)
     return rows > 16 ? 64 : rows > 4 ? 16 : 4;
 }
 
-// K parts of a product: 64-row tiles of 128 columns leave compute units idle
-// below 256 of them, so K is split until there are as many, each part keeping
-// at least four steps of 256.
+int64_t w4_tiles64(const W4Args &a) { return a.E ? (a.E < a.M ? a.E : a.M) : (a.M + 63) / 64; }
+
+// K parts of a product: where tiles of 64 rows by 64 columns leave compute
+// units idle, K is split between those of 64 x 128 until there are as many,
+// each part keeping at least four steps of 256.
 static int parts_of(const W4Args &a)
 {
-    if (a.E || w4_rows(a) < 64)
+    if (a.E || w4_rows(a) < 64 || w4_tiles64(a) * ((a.N + 63) / 64) >= 256)
         return 1;
-    const int64_t tiles = int64_t((a.N + 127) / 128) * ((a.M + 63) / 64), steps = (a.K + 255) / 256;
+    const int64_t tiles = w4_tiles64(a) * ((a.N + 127) / 128), steps = (a.K + 255) / 256;
     int parts = 1;
     while (parts < 8 && tiles * parts < 256 && steps / (2 * parts) >= 4)
         parts *= 2;
@@ -67,7 +76,7 @@ hipError_t launch_w4(const W4Args &args, hipStream_t stream)
     if (a.parts == 1 || e != hipSuccess)
         return e;
     const int steps = (a.K + 255) / 256, per = (steps + a.parts - 1) / a.parts, parts = (steps + per - 1) / per;
-    const dim3 grid((a.N + 255) / 256, a.M);
+    const dim3 grid((a.N + 1023) / 1024, a.M);
     if (a.out == kOutF32)
         hipLaunchKernelGGL((w4_reduce_kernel<kOutF32>), grid, dim3(256), 0, stream, a.ws, a.D, a.M, a.N, a.ldd, parts, a.beta);
     else if (a.bf16)

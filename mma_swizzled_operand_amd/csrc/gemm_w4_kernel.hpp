@@ -209,7 +209,10 @@ w4_kernel(W4Kernel p)
     constexpr int kStageBytes = kABytes + (E2M1 ? 1 : 2) * kSBytes;
     // one named array per stage: the compiler then knows which stage a copy
     // writes, and waits for no other one
-    constexpr int kStages = STAGES, kAhead = STAGES - 1;   // LDS stages and register slots; steps in flight
+    // LDS stages and register slots; steps in flight.  (Three stages leave room
+    // for a second or third workgroup: one row by 16384 x 8192 with two, three,
+    // four: 18.9, 15.2, 15.8 us)
+    constexpr int kStages = STAGES, kAhead = STAGES - 1;
     static_assert(STAGES >= 2 && STAGES <= 8, "named stages");
 #define W4_STAGE(i) \
     __shared__ __attribute__((aligned(1024))) uint8_t st##i[i < STAGES ? kStageBytes : 4];
@@ -575,19 +578,23 @@ hipError_t launch_w4_cols(const W4Args &a, hipStream_t stream)
     // (with 128 columns a stage has room for 16 rows as it is; 16 rows by 16
     // columns fill a compute unit's LDS, so more than one such workgroup each
     // would be a second round)
-    return enough(128, 512)                      ? launch_w4_tile<BF16, E2M1, SPAN, 16, 2, 4, 4>(a, stream)
-           : enough(64, 256)                     ? launch_w4_tile<BF16, E2M1, SPAN, ROWS, 2, 2, 4>(a, stream)
-           : enough(32, ROWS == 16 ? 129 : 256) ? launch_w4_tile<BF16, E2M1, SPAN, ROWS, 1, 2, 4>(a, stream)
-                                                 : launch_w4_tile<BF16, E2M1, SPAN, ROWS, 1, 1, 4>(a, stream);
+    return enough(128, 512)                      ? launch_w4_tile<BF16, E2M1, SPAN, 16, 2, 4, 3>(a, stream)
+           : enough(64, 256)                     ? launch_w4_tile<BF16, E2M1, SPAN, ROWS, 2, 2, 3>(a, stream)
+           : enough(32, ROWS == 16 ? 129 : 256) ? launch_w4_tile<BF16, E2M1, SPAN, ROWS, 1, 2, 3>(a, stream)
+                                                 : launch_w4_tile<BF16, E2M1, SPAN, ROWS, 1, 1, 3>(a, stream);
 }
 
 template <bool BF16, bool E2M1, int SPAN>
 hipError_t launch_w4_span(const W4Args &a, hipStream_t stream)
 {
     const int rows = w4_rows(a);
+    // 64 rows by 128 columns, K split over workgroups where those are too few;
+    // by 64 where these alone fill the chip (64 rows by 16384 x 8192, FP4: 27.1
+    // us, against 23.4 and the sum over two parts of K, 4.9)
     if (rows == 64)
-        return a.parts > 1 ? launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 4, 4, true>(a, stream)
-                           : launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 4, 4>(a, stream);
+        return a.parts > 1                                  ? launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 4, 3, true>(a, stream)
+               : w4_tiles64(a) * ((a.N + 63) / 64) >= 512 ? launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 4, 3>(a, stream)
+                                                            : launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 2, 2>(a, stream);
     return rows == 16 ? launch_w4_cols<BF16, E2M1, SPAN, 16>(a, stream) : launch_w4_cols<BF16, E2M1, SPAN, 4>(a, stream);
 }
 #endif

@@ -113,6 +113,16 @@ W4_CASES = [  # M, N, K, G, a, w, d, zeros
     (130, 17, 96, 32, "bf16", "e2m1", "f32", False),
     (1, 8192, 8192, 64, "bf16", "u4", "f32", True),
     (2, 9000, 2048, 128, "f16", "u4", "f32", True),
+    # each width of a workgroup, with and without K split over workgroups
+    (3, 16500, 1088, 128, "bf16", "u4", "f32", True),
+    (16, 16500, 544, 32, "f16", "e2m1", "f32", False),
+    (15, 4100, 1152, 64, "f16", "u4", "f16", True),
+    (2, 65700, 288, 32, "bf16", "u4", "bf16", True),
+    (40, 16400, 416, 128, "bf16", "u4", "f32", True),
+    (64, 16400, 1056, 32, "bf16", "e2m1", "f32", False),
+    (50, 32900, 96, 32, "f16", "u4", "f32", True),
+    (64, 300, 8192, 32, "f16", "e2m1", "f32", False),
+    (64, 1000, 6176, 128, "f16", "u4", "f16", True),
 ]
 
 
@@ -155,6 +165,8 @@ W4_EXPERTS = [  # counts, rows, N, K, G, a, w, d
     ([130, 1, 0, 0], 131, 33, 96, 64, "f16", "u4", "f16"),
     ([2] * 70, 150, 32, 128, 32, "bf16", "e2m1", "f32"),
     ([0, 0, 0], 4, 32, 64, 32, "f16", "e2m1", "f16"),
+    ([70, 0, 100, 33, 64], 280, 6600, 160, 64, "bf16", "u4", "f32"),
+    ([1, 3, 0, 9, 16, 17, 2, 5] * 4, 220, 2100, 320, 128, "f16", "u4", "f16"),
 ]
 
 
@@ -239,6 +251,9 @@ GROUPED = [  # counts, rows, N, K, dt, d
     ([3] * 100, 333, 40, 136, "bf16", "f32"),
     ([0, 0], 5, 16, 128, "bf16", "f32"),
     ([64, 128, 65, 1, 190], 448, 776, 320, "bf16", "bf16"),
+    # more tiles than a round of workgroups holds, with a full and with a halved last one
+    ([2100, 1900], 4000, 2304, 64, "bf16", "bf16"),
+    ([4100, 0, 4090], 8200, 2304, 72, "f16", "f32"),
 ]
 
 
