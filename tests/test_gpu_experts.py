@@ -387,6 +387,9 @@ MOE = [  # T, topk, E, H, dt, share of ids outside
     (9000, 8, 128, 64, "bf16", 0.02),
     (40, 33, 7, 2064, "bf16", 0.1),
     (20, 4, 4, 64, "f32", 1.0),
+    (1024, 8, 300, 8, "bf16", 0.01),    # the most choices that the sort does not count first
+    (8193, 1, 70, 16, "f16", 0.0),
+    (2100, 8, 1000, 8, "bf16", 0.05),
 ]
 
 
