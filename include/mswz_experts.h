@@ -103,7 +103,8 @@ enum { MSWZ_GROUP_M = 0, MSWZ_GROUP_K = 1 };
  *   d_dt  MSWZ_DT_F32 or dt
  * Rows are 16-byte aligned: K % 8 == 0 for K-major operands, N % 8 == 0, and
  * M % 8 == 0 for MSWZ_GROUP_K; an operand's [K][N] or [K][M] matrix is below
- * 4 GiB.
+ * 4 GiB, and D has fewer than 2^23 - 256 tiles of 256 x 256, counted for
+ * MSWZ_GROUP_M as if every expert's last tile were partly filled.
  * Returns MSWZ_OK, MSWZ_ERR_INVALID or MSWZ_ERR_UNSUPPORTED.
  */
 int gemm_grouped_plan_create(gemm_grouped_plan **out, int64_t E, int64_t M, int64_t N, int64_t K,

@@ -135,9 +135,10 @@ int gemm_grouped_plan_create(gemm_grouped_plan **out, int64_t E, int64_t M, int6
         return MSWZ_ERR_UNSUPPORTED;
     if ((b_mn && K * N * 2 >= kMaxBytes) || (k_axis && K * M * 2 >= kMaxBytes))
         return MSWZ_ERR_UNSUPPORTED;
-    // the launch's workgroups, one per tile of 256 x 256 at most
+    // a launch has fewer than 2^32 threads: 512 for each tile of 256 x 256 and
+    // for at most 135 workgroups that find none
     const int64_t tiles_n = (N + 255) / 256, tiles_m = k_axis ? E * ((M + 255) / 256) : mswz::most_tiles(E, M, 256);
-    if (tiles_m * tiles_n >= int64_t(1) << 30)
+    if (tiles_m * tiles_n > (int64_t(1) << 23) - 256)
         return MSWZ_ERR_UNSUPPORTED;
     gemm_grouped_plan *p = new (std::nothrow) gemm_grouped_plan{};
     if (!p)

@@ -123,6 +123,17 @@ def test_moe_plan(args, expect):
         mswz.load().moe_plan_destroy(h)
 
 
+def test_grouped_plan_beyond_a_launch():
+    """512 threads for every tile of 256 x 256: 2^23 of them are one launch too many."""
+    tiles = (1 << 23) - 256
+    most = (tiles // 4096 - 8) * 256 + 255   # rows of 8 experts, 4096 tiles side by side
+    assert create("gemm_grouped_plan", 8, most, 1 << 20, 264, F16, F16, 0, K_)[0] == 0
+    assert create("gemm_grouped_plan", 8, most + 1, 1 << 20, 264, F16, F16, 0, K_)[0] == -2
+    # along K every expert has all the tiles of its matrix
+    assert create("gemm_grouped_plan", 15, 1 << 18, 1 << 17, 8, BF16, F32, 1, MN)[0] == 0
+    assert create("gemm_grouped_plan", 16, 1 << 18, 1 << 17, 8, BF16, F32, 1, MN)[0] == -2
+
+
 def test_null_plans_and_out_pointers():
     lib = mswz.load()
     assert lib.gemm_w4_plan_create(None, 1, 16, 1024, 0, BF16, U4, BF16, 128, 0, 0) == -1
