@@ -54,7 +54,11 @@ class _Plan:
     def _create(self, *args):
         from . import MswzError, load
         lib, h = load(), ctypes.c_void_p()
-        rc = getattr(lib, self._make)(ctypes.byref(h), *args)
+        make = getattr(lib, self._make)
+        # (ctypes would cut a number off to the argument's bits)
+        if any(t(v).value != v for t, v in zip(make.argtypes[1:], args)):
+            raise MswzError(-1, self._make)
+        rc = make(ctypes.byref(h), *args)
         if rc != 0:
             raise MswzError(rc, self._make)
         self._lib, self._h = lib, h

@@ -222,3 +222,16 @@ def test_binding_refusals():
     plan.destroy()
     with pytest.raises(ValueError):
         plan.handle
+
+
+@pytest.mark.parametrize("make", [
+    lambda wide: mswz.gemm_w4_plan_create(4, 16, 256, group=128 + (wide << 32)),
+    lambda wide: mswz.gemm_w4_plan_create(4 + (wide << 64), 16, 256),
+    lambda wide: mswz.gemm_grouped_plan_create(2, 64, 64, 64 + (wide << 64)),
+    lambda wide: mswz.moe_plan_create(4, 2, 8, 64, ldx=64 + (wide << 64)),
+])
+def test_numbers_wider_than_the_argument_are_refused(make):
+    make(0)
+    for wide in (1, -1):
+        with pytest.raises(mswz.MswzError):
+            make(wide)
