@@ -280,10 +280,29 @@ w4_kernel(W4Kernel p)
         a_off[i] = m < rows ? uint32_t(m * p.lda + a_k[i]) * 2 : a_bytes;
     }
 
-    u32x4 w[kStages][NB];
-    // all loads of step t (a step beyond the last repeats it: never used)
-    auto load = [&](int slot, uint8_t *st, int t) __attribute__((always_inline)) {
-        const int c0 = (first + min(t, steps - 1)) * KQ;          // first chunk of the step
+    // Step t's place along K.  Workgroups that share an XCD's L2 start at
+    // different places, as they all read the same rows of A, whose pieces at one
+    // place lie in few channels of the L2 if the pitch is a power of two (64
+    // rows by 16384 x 8192, FP4: 26.5 us without, 25.6).
+    const int turn = ROWS > 4 ? int(blockIdx.x >> 3) % steps : 0;
+    auto chunk_of = [&](int t) __attribute__((always_inline)) {   // first chunk of the step
+        const int at = t + turn;
+        return (first + (ROWS > 4 && at >= steps ? at - steps : at)) * KQ;
+    };
+    // Two stages leave a step's weights, which come from memory, little time:
+    // they are loaded one step earlier than A and the scales, before those of
+    // the step between (28.0 -> 26.5 us; with three stages no gain).
+    constexpr int kEarly = STAGES == 2, kSlots = kEarly ? 2 * kStages : kStages;
+    u32x4 w[kSlots][NB];
+    // the loads of step t (a step beyond the last repeats it: never used)
+    auto load_w = [&](int slot, int t) __attribute__((always_inline)) {
+        const uint32_t kb = uint32_t(chunk_of(min(t, steps - 1))) * 64;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+            w[slot][nb] = buffer_load16(rw, w_off[nb] + kb, 0);
+    };
+    auto load_as = [&](uint8_t *st, int t) __attribute__((always_inline)) {
+        const int c0 = chunk_of(min(t, steps - 1));
         const uint32_t kb = uint32_t(c0) * 64;
         const int left = p.K - c0 * kChunk;     // K values from the step's first on
 #pragma unroll
@@ -294,9 +313,12 @@ w4_kernel(W4Kernel p)
         for (int i = 0; i < kSCopies; ++i)
             buffer_load_lds4(rs, st + kABytes + (zeros ? kSBytes : 0) + 4 * (kSThreads * i + 64 * (wave % (kSThreads / 64))),
                              ((s_off[i] + g0) & ~3u) + s_word[i], 0);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-            w[slot][nb] = buffer_load16(rw, w_off[nb] + kb, 0);
+    };
+    auto load = [&](int u, int t) __attribute__((always_inline)) {   // (u = t modulo the stages and the slots)
+        load_as(stage(u % kStages), t);
+        if constexpr (kEarly)
+            sched_fence();
+        load_w((u + kEarly) % kSlots, t + kEarly);
     };
     constexpr int kLoads = kCopies + kSCopies + NB;   // vector-memory operations of one step
 
@@ -334,7 +356,7 @@ w4_kernel(W4Kernel p)
     const uint32_t s_place = uint32_t(kABytes + 4 * kSWords * (16 * NB * ng + r) + (kPre ? q : 0));
     const uint32_t z_place = uint32_t(kABytes + kSBytes + 4 * kZWords * (16 * NB * ng + r));
     auto scales = [&](const uint8_t *st, int t, int nb, uint32_t *sv, uint32_t *zv) __attribute__((always_inline)) {
-        const int c0 = (first + t) * KQ, g0 = group_of(c0), g1 = group_of(c0 + kq);
+        const int c0 = chunk_of(t), g0 = group_of(c0), g1 = group_of(c0 + kq);
         const uint32_t s_at = ((s_mod[nb] + uint32_t(g0) * kSize) & 3) + (s_place + uint32_t(g1 - g0) * kSize);
 #pragma unroll
         for (int g = 0; g < kSpans; ++g) {
@@ -469,24 +491,28 @@ w4_kernel(W4Kernel p)
         }
     };
 
-    // Step t: wait until its own loads have landed (the kAhead - 1 later steps'
-    // may stay in flight), barrier (every wave's copies are in LDS, and all
+    // Step t: wait until its own loads have landed (the kAhead - 1 later steps',
+    // and weights that are loaded early, may stay in flight), barrier (every wave's copies are in LDS, and all
     // have read the stage that is filled next), compute, load step t + kAhead.
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-        load(u, stage(u), u);
+    if constexpr (kEarly) {
+        load_w(0, 0);
         sched_fence();
     }
-    // (Whole rounds of stages without a branch, then the rest: with an exit in
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+        load(u, u);
+        sched_fence();
+    }
+    // (Whole rounds of slots without a branch, then the rest: with an exit in
     // every step the loop's registers had to be copied on the way round, which
     // waited for all loads in flight.)
     auto step = [&](auto uc, int t) __attribute__((always_inline)) {
         constexpr int u = decltype(uc)::value;
-        lds_barrier_keep_vm<(kAhead - 1) * kLoads>();
+        lds_barrier_keep_vm<(kAhead - 1) * kLoads + kEarly * NB>();
         sched_fence();
-        load((u + kAhead) % kStages, stage((u + kAhead) % kStages), t + kAhead);
+        load(u + kAhead, t + kAhead);
         sched_fence();
-        compute(stage(u), u, t);
+        compute(stage(u % kStages), u, t);
         // (the sums are finished here: left open, several steps' products were
         // kept in registers until the last one's scales came)
 #pragma unroll
@@ -497,9 +523,9 @@ w4_kernel(W4Kernel p)
         sched_fence();
     };
     int t = 0;
-    for (; t + kStages <= steps; t += kStages)
-        static_for<0, kStages>([&](auto uc) __attribute__((always_inline)) { step(uc, t + decltype(uc)::value); });
-    static_for<0, kStages - 1>([&](auto uc) __attribute__((always_inline)) {
+    for (; t + kSlots <= steps; t += kSlots)
+        static_for<0, kSlots>([&](auto uc) __attribute__((always_inline)) { step(uc, t + decltype(uc)::value); });
+    static_for<0, kSlots - 1>([&](auto uc) __attribute__((always_inline)) {
         if (t + decltype(uc)::value < steps)
             step(uc, t + decltype(uc)::value);
     });
@@ -589,8 +615,8 @@ hipError_t launch_w4_span(const W4Args &a, hipStream_t stream)
 {
     const int rows = w4_rows(a);
     // 64 rows by 128 columns, K split over workgroups where those are too few;
-    // by 64 where these alone fill the chip (64 rows by 16384 x 8192, FP4: 27.1
-    // us, against 23.4 and the sum over two parts of K, 4.9)
+    // by 64 where these alone fill the chip (64 rows by 16384 x 8192, FP4: 25.6
+    // us, against 22.6 and the sum over two parts of K, 4.9)
     if (rows == 64)
         return a.parts > 1                                  ? launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 4, 3, true>(a, stream)
                : w4_tiles64(a) * ((a.N + 63) / 64) >= 512 ? launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 4, 3>(a, stream)
