@@ -146,9 +146,12 @@ __device__ __forceinline__ int w4_piece(int j, int q)
 // two lane groups' pieces, whose numbers differ in bit 2 (bit 0 for 32-value
 // spans).  The key takes the other three bits from the eight rows, so that the
 // sixteen reads fall into different banks.
-template <int SPAN>
+// (Four rows: two lane groups and four rows, plain keys.)
+template <int SPAN, int ROWS>
 __host__ __device__ constexpr int row_key(int m)
 {
+    if (ROWS == 4)
+        return SPAN == 32 ? m << 1 : m;
     return SPAN == 32 ? (m & 1) << 1 | (m & 2) >> 1 | (m & 12) : (m & 1) | (m & 4) >> 1 | (m & 2) << 1 | (m & 8);
 }
 
@@ -211,7 +214,7 @@ w4_kernel(W4Kernel p)
     // writes, and waits for no other one
     // LDS stages and register slots; steps in flight.  (Three stages leave room
     // for a second or third workgroup: one row by 16384 x 8192 with two, three,
-    // four: 18.9, 15.2, 15.8 us)
+    // four: 18.4, 14.1, 14.6 us)
     constexpr int kStages = STAGES, kAhead = STAGES - 1;
     static_assert(STAGES >= 2 && STAGES <= 8, "named stages");
 #define W4_STAGE(i) \
@@ -276,7 +279,7 @@ w4_kernel(W4Kernel p)
     for (int i = 0; i < kCopies; ++i) {
         // unit u of the stage: [row][piece's place]
         const int u = tid + kW4Threads * i, m = u / (16 * KQ);
-        a_k[i] = 8 * (u % (16 * KQ) ^ row_key<SPAN>(m));
+        a_k[i] = 8 * (u % (16 * KQ) ^ row_key<SPAN, ROWS>(m));
         a_off[i] = m < rows ? uint32_t(m * p.lda + a_k[i]) * 2 : a_bytes;
     }
 
@@ -294,17 +297,19 @@ w4_kernel(W4Kernel p)
     // the step between (28.0 -> 26.5 us; with three stages no gain).
     constexpr int kEarly = STAGES == 2, kSlots = kEarly ? 2 * kStages : kStages;
     u32x4 w[kSlots][NB];
-    // the loads of step t (a step beyond the last repeats it: never used)
+    // the loads of step t (beyond the last they lie outside the buffers' ranges:
+    // repeating the last step's cost its traffic once more per stage)
     auto load_w = [&](int slot, int t) __attribute__((always_inline)) {
-        const uint32_t kb = uint32_t(chunk_of(min(t, steps - 1))) * 64;
+        const uint32_t kb = uint32_t(chunk_of(t)) * 64;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
-            w[slot][nb] = buffer_load16(rw, w_off[nb] + kb, 0);
+            w[slot][nb] = buffer_load16(rw, t < steps ? w_off[nb] + kb : w_bytes, 0);
     };
     auto load_as = [&](uint8_t *st, int t) __attribute__((always_inline)) {
         const int c0 = chunk_of(min(t, steps - 1));
+        const bool past = t >= steps;
         const uint32_t kb = uint32_t(c0) * 64;
-        const int left = p.K - c0 * kChunk;     // K values from the step's first on
+        const int left = past ? 0 : p.K - c0 * kChunk;     // K values from the step's first on
 #pragma unroll
         for (int i = 0; i < kCopies; ++i)
             buffer_load_lds16(ra, st + 16 * (kW4Threads * i + 64 * wave), a_k[i] < left ? a_off[i] + kb * 4 : a_bytes, 0);
@@ -312,7 +317,7 @@ w4_kernel(W4Kernel p)
 #pragma unroll
         for (int i = 0; i < kSCopies; ++i)
             buffer_load_lds4(rs, st + kABytes + (zeros ? kSBytes : 0) + 4 * (kSThreads * i + 64 * (wave % (kSThreads / 64))),
-                             ((s_off[i] + g0) & ~3u) + s_word[i], 0);
+                             past ? 0x80000000u : ((s_off[i] + g0) & ~3u) + s_word[i], 0);
     };
     auto load = [&](int u, int t) __attribute__((always_inline)) {   // (u = t modulo the stages and the slots)
         load_as(stage(u % kStages), t);
@@ -322,18 +327,26 @@ w4_kernel(W4Kernel p)
     };
     constexpr int kLoads = kCopies + kSCopies + NB;   // vector-memory operations of one step
 
-    f32x4 acc[NB][MB];
+    // Lane (r, q) gets rows 4q .. 4q + 3 of the MFMA's result.  A tile of four
+    // rows gives the MFMA each of them four times, row q in rows 4q .. 4q + 3,
+    // so that a lane has one sum to scale instead of four (32 experts of 4096
+    // x 2048, groups of 32: 46.7 -> 43.8 us; one row by 16384 x 8192: 14.0 ->
+    // 13.5).
+    constexpr int kSame = ROWS == 4 ? 4 : 1, kRegs = ROWS == 4 && !kPre ? 1 : 4;
+    using Acc = std::conditional_t<kRegs == 1, float, f32x4>;
+    Acc acc[NB][MB];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
-            acc[nb][mb] = f32x4{};
+            acc[nb][mb] = Acc{};
     const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 
     // A's fragments: the lane's piece of row r for MFMA j and row block mb, i.e.
     // one base, XOR a constant of j, plus one of mb (opaque: else every sum of
     // them is kept in a register of its own through the loop)
-    const uint32_t a_base = 16u * uint32_t((r % ROWS * KQ + kq) * 16 + (w4_piece<SPAN>(0, q) ^ row_key<SPAN>(r % ROWS)));
+    const int a_row = ROWS == 4 ? r >> 2 : r;
+    const uint32_t a_base = 16u * uint32_t((a_row * KQ + kq) * 16 + (w4_piece<SPAN>(0, q) ^ row_key<SPAN, ROWS>(a_row)));
     auto pieces = [&](const uint8_t *st, int j, u32x4 *av) __attribute__((always_inline)) {
         const uint32_t at = opaque(a_base ^ uint32_t(16 * w4_piece<SPAN>(j, 0)));
 #pragma unroll
@@ -484,9 +497,12 @@ w4_kernel(W4Kernel p)
 #pragma unroll
                 for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < kRegs; ++i) {
                         const float v = kSums ? __builtin_fmaf(-zero[nb], sum[mb][i], part[nb][mb][i]) : part[nb][mb][i];
-                        acc[nb][mb][i] = __builtin_fmaf(scale[nb], v, acc[nb][mb][i]);
+                        if constexpr (kRegs == 1)
+                            acc[nb][mb] = __builtin_fmaf(scale[nb], v, acc[nb][mb]);
+                        else
+                            acc[nb][mb][i] = __builtin_fmaf(scale[nb], v, acc[nb][mb][i]);
                     }
         }
     };
@@ -533,18 +549,24 @@ w4_kernel(W4Kernel p)
 
     // sums over the KQ waves of a column block: tile tl of column block ng is
     // added up, in wave order, by one of them (waves 0-3 leave theirs in stage
-    // 0, 4-7 in stage 1); lane holds column r of the 16, rows 4q .. 4q+3
+    // 0, 4-7 in stage 1); lane holds column r of the 16, rows 4q .. 4q+3 (of
+    // four rows, row q)
+    using Out = std::conditional_t<kSame == 4, float, f32x4>;
     auto sums = [&](int wv, int tl) {
-        return reinterpret_cast<f32x4 *>((wv < 4 ? st0 : st1) + (((wv & 3) * NB * MB + tl) * 64 + lane) * 16);
+        return reinterpret_cast<Out *>((wv < 4 ? st0 : st1) + (((wv & 3) * NB * MB + tl) * 64 + lane) * sizeof(Out));
     };
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-            *sums(wave, nb * MB + mb) = acc[nb][mb];
+        for (int mb = 0; mb < MB; ++mb) {
+            if constexpr (kSame == 4 && kRegs == 4)
+                *sums(wave, nb * MB + mb) = acc[nb][mb][0];
+            else
+                *sums(wave, nb * MB + mb) = acc[nb][mb];
+        }
     __syncthreads();
     for (int tl = kq; tl < NB * MB; tl += KQ) {
-        f32x4 sum = *sums(ng, tl);
+        Out sum = *sums(ng, tl);
 #pragma unroll
         for (int x = 1; x < KQ; ++x)
             sum += *sums(NG * x + ng, tl);
@@ -552,17 +574,22 @@ w4_kernel(W4Kernel p)
         if (n >= p.N)
             continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = 16 * mb + 4 * q + i;
+        for (int i = 0; i < 4 / kSame; ++i) {
+            const int m = 16 * mb + 4 / kSame * q + i;
             if (m >= rows)
                 continue;
+            float v;
+            if constexpr (kSame == 4)
+                v = sum;
+            else
+                v = sum[i];
             if constexpr (SPLIT) {
-                p.ws[(size_t(blockIdx.z) * p.M + m0 + m) * p.N + n] = sum[i];
+                p.ws[(size_t(blockIdx.z) * p.M + m0 + m) * p.N + n] = v;
             } else {
                 const size_t at = size_t(m0 + m) * p.ldd + n;
                 using T = std::conditional_t<OUT == kOutF32, float, std::conditional_t<OUT == kOutBf16, __bf16, _Float16>>;
                 T *d = static_cast<T *>(p.D) + at;
-                *d = T(p.beta ? sum[i] + float(*d) : sum[i]);
+                *d = T(p.beta ? v + float(*d) : v);
             }
         }
     }
@@ -593,18 +620,17 @@ hipError_t launch_w4_tile(const W4Args &a, hipStream_t stream)
 // Columns of a workgroup: as many as leave a workgroup for every compute unit
 // (two, for the longest), since more columns share a copy of A and a step's
 // addresses, and make a wave's part of K and with it its run of steps longer.
-// One row by 16384 x 8192, u4: 64 columns 15.9 us, 32 in two blocks of a wave
-// 18.5, 32 in two waves 16.9, 128 (half the units) 37; by 4096 x 4096: 16
-// columns 4.3 us, 32 6.2.
+// One row by 16384 x 8192, u4, when chosen: 64 columns 15.9 us (now 13.5), 32
+// in two blocks of a wave 18.5, 32 in two waves 16.9, 128 (half the units) 37;
+// by 4096 x 4096: 16 columns 4.3 us, 32 6.2.
 template <bool BF16, bool E2M1, int SPAN, int ROWS>
 hipError_t launch_w4_cols(const W4Args &a, hipStream_t stream)
 {
     const int64_t tiles = a.E ? (a.E < a.M ? a.E : a.M) : 1;
     auto enough = [&](int cols, int wgs) { return tiles * ((a.N + cols - 1) / cols) >= wgs; };
-    // (with 128 columns a stage has room for 16 rows as it is; 16 rows by 16
-    // columns fill a compute unit's LDS, so more than one such workgroup each
-    // would be a second round)
-    return enough(128, 512)                      ? launch_w4_tile<BF16, E2M1, SPAN, 16, 2, 4, 3>(a, stream)
+    // (16 rows by 16 columns fill a compute unit's LDS, so more than one such
+    // workgroup each would be a second round)
+    return enough(128, 512)                      ? launch_w4_tile<BF16, E2M1, SPAN, ROWS, 2, 4, 3>(a, stream)
            : enough(64, 256)                     ? launch_w4_tile<BF16, E2M1, SPAN, ROWS, 2, 2, 3>(a, stream)
            : enough(32, ROWS == 16 ? 129 : 256) ? launch_w4_tile<BF16, E2M1, SPAN, ROWS, 1, 2, 3>(a, stream)
                                                  : launch_w4_tile<BF16, E2M1, SPAN, ROWS, 1, 1, 3>(a, stream);
