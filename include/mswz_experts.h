@@ -8,7 +8,8 @@
  * on `stream` (which must belong to the current device) and returns; it
  * allocates nothing, does not synchronise, keeps no pointer and can be
  * captured into a graph; results are bit-identical run to run.  Matrices are
- * row-major, device memory.
+ * row-major, device memory; what a call writes must not overlap what it reads
+ * or writes elsewhere (D itself is read where beta is 1).
  *
  * A layer of experts is moe_dispatch (tokens to sorted rows), products over
  * the sorted rows (gemm_run_grouped, or gemm_run_w4 with 4-bit weights) and
@@ -19,9 +20,10 @@
  * Sorted rows.  `offsets`, int32 [E+1] in device memory, bounds the groups:
  * rows offsets[e] .. offsets[e+1] - 1 belong to expert e.  Row counts are
  * known on the device only; the plan's M is the capacity.  Bounds are clamped
- * to 0 .. M and a group whose bounds descend is empty, so no value of them
- * reads or writes outside the buffers.  Rows outside every group are neither
- * read nor written.
+ * to 0 .. M (K for MSWZ_GROUP_K) and a group whose bounds descend is empty, so
+ * no value of them reads or writes outside the buffers; what groups that
+ * overlap leave in D is not defined.  Rows outside every group are neither read
+ * nor written.
  */
 #ifndef MSWZ_EXPERTS_H
 #define MSWZ_EXPERTS_H
@@ -63,8 +65,10 @@ typedef struct moe_plan moe_plan;
  *             lda % 8 == 0, both at most 2^22
  * Storage: A [M][K]; B uint8 [E][N][K/2] (two elements a byte); S and Z
  * [E][N][ceil(K/group)]; without experts one matrix, E = 1 in these shapes.
- * The 4-bit integers, z and the products enter exactly; sums are fp32.  With
- * bf16 A and U4 weights a row of A holding an infinity gives NaN.
+ * The 4-bit integers, z and the products enter exactly; sums are fp32, and a
+ * group's sum is formed before its scale.  With bf16 A and U4 weights that is
+ * the sum of A w less z times the sum of A: a row of A holding an infinity, or
+ * values whose sums leave fp32's range, gives NaN.
  * Returns MSWZ_OK, MSWZ_ERR_INVALID or MSWZ_ERR_UNSUPPORTED.
  */
 int gemm_w4_plan_create(gemm_w4_plan **out, int64_t M, int64_t N, int64_t K, int64_t E, int a_dt,
@@ -76,10 +80,12 @@ int64_t gemm_w4_plan_workspace_size(const gemm_w4_plan *plan);
 
 /*
  * Enqueue the product.  A, B and workspace are 16-byte aligned, S and D
- * aligned to their elements; Z may be NULL (U4) and is NULL for E2M1; offsets is NULL exactly for
- * a plan without experts; beta is 0 or 1.  The workspace (NULL where
- * none is needed) is the caller's, its contents before the call do not
- * matter, and calls that may overlap must not share it.
+ * aligned to their elements (the whole 4-byte words that hold their first and
+ * last bytes are read); Z may be NULL (U4) and is NULL for E2M1; offsets is
+ * NULL exactly for a plan without experts; beta is 0 or 1.  The workspace (NULL
+ * where none is needed) is the caller's, its contents before the call do not
+ * matter, and calls that may overlap must not share it, replays of two captured
+ * graphs among them.
  * Returns MSWZ_OK, MSWZ_ERR_INVALID, MSWZ_ERR_ALIGN or MSWZ_ERR_HIP.
  */
 int gemm_run_w4(const gemm_w4_plan *plan, const void *A, const void *B, const void *S,

@@ -40,7 +40,9 @@ w4_reduce_kernel(const float *__restrict__ ws, void *__restrict__ D, int M, int 
 
 int w4_rows(const W4Args &a)
 {
-    // rows that a tile is expected to hold: experts share them
+    // rows that a tile is expected to hold: experts share them (16384 x 8192, u4:
+    // one row in tiles of 4 takes 13.5 us, 16 in tiles of 16 15.9, 64 in tiles
+    // of 64 30)
     const int64_t rows = a.E ? (int64_t(a.M) + a.E - 1) / a.E : a.M;
     return rows > 16 ? 64 : rows > 4 ? 16 : 4;
 }
@@ -49,7 +51,9 @@ int64_t w4_tiles64(const W4Args &a) { return a.E ? (a.E < a.M ? a.E : a.M) : (a.
 
 // K parts of a product: where tiles of 64 rows by 64 columns leave compute
 // units idle, K is split between those of 64 x 128 until there are as many,
-// each part keeping at least four steps of 256.
+// each part keeping at least four steps of 256.  (64 rows by 16384 x 8192, when
+// tiles of 128 columns were the only ones: 52 us unsplit, 32 and 4.9 for the sum
+// in two parts.)
 static int parts_of(const W4Args &a)
 {
     if (a.E || w4_rows(a) < 64 || w4_tiles64(a) * ((a.N + 63) / 64) >= 256)

@@ -208,7 +208,8 @@ moe_place_kernel(const int32_t *__restrict__ ids, int n, int E, int bits, const 
 // finds the rows of token t's choices by counting the choices before them
 // (smaller expert, or the same expert earlier), all of them from one read of
 // ids, and copies its piece of the row; workgroup T writes offsets and the
-// places behind the last group, from a histogram.
+// places behind the last group, from a histogram.  (1024 choices 5.0 us in a
+// graph; in two launches 2048 take 8.4.)
 __global__ void __launch_bounds__(256)
 moe_few_kernel(const int32_t *__restrict__ ids, const u32x4 *__restrict__ X, u32x4 *__restrict__ Xs, int T, int topk,
                int E, int vecs, int64_t ldx16, int32_t *__restrict__ offsets, int32_t *__restrict__ order,

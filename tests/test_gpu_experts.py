@@ -185,6 +185,58 @@ def test_w4_experts(counts, rows, N, K, G, a, w, d):
     assert (got[used:] == GUARD).all()
 
 
+@pytest.mark.parametrize("counts,N,a,w", [([2, 0, 3], 37, "bf16", "u4"), ([9, 20, 1], 37, "f16", "u4"), ([2, 1, 1], 67, "bf16", "e2m1"),
+                                          ([40, 30, 1], 70, "f16", "e2m1")])
+def test_w4_scales_at_any_alignment(counts, N, a, w):
+    """Scales and zero points that start and end between words, NaN and 255 around them."""
+    M, K, E = sum(counts), 160, 3
+    x, bounds = w4_inputs(gen(N + M), M, N, K, E, a, w, 32, w == "u4"), bounds_of(counts)
+    ref, mag = w4_reference(x, w, 32, a, bounds.tolist())
+    plan = mswz.gemm_w4_plan_create(M, N, K, a, w, "f32", group=32, experts=E)
+    ws = torch.empty(max(16, plan.workspace_bytes()), dtype=torch.uint8, device="cuda")
+
+    def inside(t, off):
+        wide = torch.full((t.numel() + 8,), float("nan") if t.dtype.is_floating_point else 255, dtype=t.dtype)
+        wide[off:off + t.numel()] = t.reshape(-1)
+        return wide.cuda()[off:off + t.numel()]
+
+    for off in (1, 2, 3, 5):
+        D = torch.full((M, N), float("nan"), device="cuda")
+        mswz.gemm_run_w4(plan, x["A"].cuda(), x["B"].cuda(), inside(x["S"], off), D, Z=None if x["Z"] is None else inside(x["Z"], 6 - off),
+                         offsets=bounds.cuda(), workspace=ws)
+        check(D, ref, mag, K, "f32", off)
+
+
+def test_w4_weights_past_4_gib():
+    E, N, K = 1024, 4128, 2112
+    x = w4_inputs(gen(50), 8, N, K, 2, "bf16", "u4", 64, True)
+    B = torch.zeros(E, N, K // 2, dtype=torch.uint8, device="cuda")
+    S, Z = torch.zeros(E, N, K // 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(E, N, K // 64, dtype=torch.uint8, device="cuda")
+    for e, i in ((0, 0), (E - 1, 1)):
+        B[e], S[e], Z[e] = x["B"][i].cuda(), x["S"][i].cuda(), x["Z"][i].cuda()
+    offsets = torch.full((E + 1,), 3, dtype=torch.int32)
+    offsets[0], offsets[E] = 0, 8
+    D = torch.full((8, N), float("nan"), device="cuda")
+    plan = mswz.gemm_w4_plan_create(8, N, K, "bf16", "u4", "f32", group=64, experts=E)
+    mswz.gemm_run_w4(plan, x["A"].cuda(), B, S, D, Z=Z, offsets=offsets.cuda())
+    check(D, *w4_reference(x, "u4", 64, "bf16", [0, 3, 8]), K, "f32")
+
+
+def test_w4_rows_past_4_gib():
+    M, N, K, ld = 600, 24, 96, 1 << 22
+    x = w4_inputs(gen(51), M, N, K, 0, "bf16", "u4", 32, True)
+    A = torch.empty(M, ld, dtype=torch.bfloat16, device="cuda")
+    A[:, :K] = x["A"].cuda()
+    A[:, K:K + 64] = float("nan")
+    D = torch.empty(M, ld, dtype=torch.bfloat16, device="cuda")
+    D[:, :64] = GUARD
+    plan = mswz.gemm_w4_plan_create(M, N, K, "bf16", "u4", "bf16", group=32, lda=ld, ldd=ld)
+    ws = torch.empty(max(16, plan.workspace_bytes()), dtype=torch.uint8, device="cuda")
+    mswz.gemm_run_w4(plan, A[:, :K], x["B"].cuda(), x["S"].cuda(), D[:, :N], Z=x["Z"].cuda(), workspace=ws)
+    check(D[:, :N], *w4_reference(x, "u4", 32, "bf16"), K, "bf16")
+    assert (D[:, N:64] == GUARD).all()
+
+
 def test_w4_bounds_that_do_not_ascend_stay_inside_the_buffers():
     g = gen(3)
     x = w4_inputs(g, 8, 32, 64, 4, "bf16", "u4", 64, True)
