@@ -731,6 +731,50 @@ def test_w4_layer_captured_on_another_stream():
         assert float((Y.double().cpu() - ref).norm() / ref.norm()) <= 2 * torch.finfo(torch.bfloat16).eps / 2
 
 
+def test_two_streams_at_once():
+    """One plan of each kind, used on two streams with a workspace each."""
+    T, topk, E, H, N = 3000, 4, 24, 512, 264
+    n = T * topk
+    moe, up = mswz.moe_plan_create(T, topk, E, H, "bf16"), mswz.gemm_grouped_plan_create(E, n, N, H, "bf16", "f32")
+    plan = mswz.gemm_w4_plan_create(64, 300, 8192, "f16", "e2m1", "f32", group=32)
+    assert moe.workspace_bytes() and plan.workspace_bytes()
+
+    def state(seed):
+        g = gen(seed)
+        x = {k: v.cuda() for k, v in w4_inputs(g, 64, 300, 8192, 0, "f16", "e2m1", 32, False).items() if v is not None}
+        i32 = lambda *sh: torch.zeros(*sh, dtype=torch.int32, device="cuda")
+        return dict(x=x, ids=ids_for(g, T, topk, E, 0.1).cuda(), X=normal(g, T, H).cuda(), w=torch.rand(T, topk, generator=g).cuda(),
+                    B=normal(g, E, N, H).cuda(), offsets=i32(E + 1), order=i32(n), pos=i32(T, topk),
+                    Xs=torch.zeros(n, H, dtype=torch.bfloat16, device="cuda"), Ys=torch.zeros(n, N, device="cuda"),
+                    Y=torch.zeros(T, H, dtype=torch.bfloat16, device="cuda"), D=torch.zeros(64, 300, device="cuda"),
+                    ws=torch.zeros(moe.workspace_bytes(), dtype=torch.uint8, device="cuda"),
+                    ws4=torch.zeros(plan.workspace_bytes(), dtype=torch.uint8, device="cuda"))
+
+    def run(s, stream=None):
+        mswz.moe_dispatch(moe, s["ids"], s["X"], s["Xs"], s["offsets"], s["order"], s["pos"], s["ws"], stream=stream)
+        mswz.gemm_run_grouped(up, s["Xs"], s["B"], s["offsets"], s["Ys"], stream=stream)
+        mswz.moe_combine(moe, s["Xs"], s["pos"], s["Y"], weights=s["w"], stream=stream)
+        mswz.gemm_run_w4(plan, s["x"]["A"], s["x"]["B"], s["x"]["S"], s["D"], workspace=s["ws4"], stream=stream)
+
+    states, out = [state(60), state(61)], ("offsets", "order", "pos", "Xs", "Ys", "Y", "D")
+    alone = []
+    for s in states:
+        run(s)
+        torch.cuda.synchronize()
+        alone.append({k: s[k].clone() for k in out})
+        for k in out:
+            s[k].zero_()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, stream in zip(states, streams):
+            run(s, stream)
+    torch.cuda.synchronize()
+    for s, want in zip(states, alone):
+        for k in out:
+            assert torch.equal(s[k], want[k]), k
+
+
 def test_tensors_that_do_not_fit_are_refused():
     plan = mswz.gemm_w4_plan_create(2, 16, 64, "bf16", "u4", "f32", group=64)
     A, B = torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(16, 32, dtype=torch.uint8, device="cuda")
