@@ -12,14 +12,20 @@
 // One workgroup of eight waves owns up to ROWS rows and 16*NB*NG columns of D.
 // Its waves split the columns NG ways and K KQ ways (NG * KQ = 8): a step is
 // 128*KQ values of K, of which each wave takes 128 (64 bytes of each of its
-// weight rows).  Few rows need no sharing of A and take KQ = 8, so that a
-// workgroup requests 512 consecutive bytes of each weight row; 64 rows take
-// KQ = 2, so that A, which every workgroup reads from L2, serves more columns.
+// weight rows).  A large KQ asks for long pieces of each weight row, many
+// columns let a copy of A, which every workgroup reads from L2, serve more
+// weights; the grid decides (launch_w4_cols, launch_w4_span).
 // Weights are loaded into registers, A and the scales into an LDS stage by
 // direct copies, kAhead steps early; a step's barrier waits for its own copies
 // and leaves the later steps' loads in flight.  (Scales and zero points loaded
 // by the lanes that use them, two or three bytes each from sixteen rows, took
 // longer than the weights: one row by 16384 x 8192 in 33 us, 18 us without.)
+//
+// Now, inputs changed from call to call: one row by 16384 x 8192, U4 in groups
+// of 128, 13.5 us (68 MB at 5.1 TB/s, memory bound); 64 rows, FP4, 25.2 us (71
+// MB, and 256 MB of A from L2, which is the longer part); 32 experts of 4096 x
+// 2048 and two rows each, U4 in groups of 64, 34.2 us (125 MB at 3.7 TB/s, the
+// scales' short pieces and many short workgroups).
 //
 // Lane l = (r, q) = (l % 16, l / 16) loads 16 bytes of weight row r, K block q
 // (32 values) of the wave's 128.  MFMA j multiplies dword j of every lane.  The
