@@ -22,7 +22,7 @@
 // longer than the weights: one row by 16384 x 8192 in 33 us, 18 us without.)
 //
 // Now, inputs changed from call to call: one row by 16384 x 8192, U4 in groups
-// of 128, 13.5 us (68 MB at 5.1 TB/s, memory bound); 64 rows, FP4, 25.2 us (71
+// of 128, 13.5 us (70 MB at 5.2 TB/s, memory bound); 64 rows, FP4, 25.2 us (74
 // MB, and 256 MB of A from L2, which is the longer part); 32 experts of 4096 x
 // 2048 and two rows each, U4 in groups of 64, 34.2 us (125 MB at 3.7 TB/s, the
 // scales' short pieces and many short workgroups).
