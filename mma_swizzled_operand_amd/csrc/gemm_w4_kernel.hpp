@@ -424,12 +424,14 @@ w4_kernel(W4Kernel p)
                         f32x4 part[MB];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const u32x4 v = e2m1_values<BF16>(big && q == g ? w[slot][nb][j] : 0, 1.0f);
+                            const u32x4 v = e2m1_values<BF16>(w[slot][nb][j], 1.0f);
                             u32x4 x[MB];
                             pieces(st, j, x);
+                            // (A's other lane groups are zeroed, not their weights: an infinity
+                            // of A times a zero weight would be NaN)
 #pragma unroll
                             for (int mb = 0; mb < MB; ++mb)
-                                part[mb] = mfma_16x16x32<BF16>(x[mb], v, j ? part[mb] : f32x4{});
+                                part[mb] = mfma_16x16x32<BF16>(q == g ? x[mb] : u32x4{}, v, j ? part[mb] : f32x4{});
                         }
 #pragma unroll
                         for (int mb = 0; mb < MB; ++mb)

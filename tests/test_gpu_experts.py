@@ -794,3 +794,31 @@ def test_tensors_that_do_not_fit_are_refused():
     with pytest.raises(ValueError):
         mswz.moe_dispatch(big, i32(n), torch.zeros(5000, 8, device="cuda"), None, i32(5), i32(n), i32(n),
                           torch.zeros(1 << 20, device="cuda"))
+
+
+@pytest.mark.parametrize("a", ["bf16", "f16"])
+@pytest.mark.parametrize("M", [1, 4, 16, 40, 64])
+def test_w4_largest_e8m0_scales(M, a):
+    """Scale bytes 249 .. 254 in any block of 32, with A small enough for finite results, and an infinity of A in
+    a block whose neighbours have such scales."""
+    g, N, K = gen(70 + M), 70, 416
+    x = w4_inputs(g, M, N, K, 0, a, "e2m1", 32, False)
+    x["A"] = (torch.randn(M, K, generator=g) * 2.0 ** -20).to(DT[a])
+    x["S"] = torch.randint(249, 255, (1, N, K // 32), generator=g, dtype=torch.uint8)
+    plan = mswz.gemm_w4_plan_create(M, N, K, a, "e2m1", "f32", group=32)
+    ref, mag = w4_reference(x, "e2m1", 32, a)
+    assert float(mag.max()) < torch.finfo(torch.float32).max
+    got = w4_run(plan, x, torch.full((M, N), float("nan"), device="cuda"))
+    check(got, ref, mag, K, "f32")
+    at = torch.randint(0, K, (M,), generator=g)
+    odd = torch.arange(M) % 2 == 1 if M > 1 else torch.ones(1, dtype=torch.bool)
+    for m in torch.nonzero(odd)[:, 0].tolist():
+        x["A"][m, at[m]] = float("inf") if m % 4 == 1 else -float("inf")
+        pair = x["B"][0, :, int(at[m]) // 2]   # no zero weight meets it
+        pair[pair % 8 == 0] |= 1
+        pair[pair // 16 % 8 == 0] |= 16
+    ref, mag = w4_reference(x, "e2m1", 32, a)
+    got = w4_run(plan, x, torch.full((M, N), float("nan"), device="cuda")).cpu()
+    assert torch.isinf(ref[odd]).all()
+    assert torch.equal(got[odd].double(), ref[odd])
+    check(got[~odd], ref[~odd], mag[~odd], K, "f32")
