@@ -65,10 +65,13 @@ typedef struct moe_plan moe_plan;
  *             lda % 8 == 0, both at most 2^22
  * Storage: A [M][K]; B uint8 [E][N][K/2] (two elements a byte); S and Z
  * [E][N][ceil(K/group)]; without experts one matrix, E = 1 in these shapes.
- * The 4-bit integers, z and the products enter exactly; sums are fp32, and a
- * group's sum is formed before its scale.  With bf16 A and U4 weights that is
- * the sum of A w less z times the sum of A: a row of A holding an infinity, or
- * values whose sums leave fp32's range, gives NaN.
+ * The 4-bit integers, z and the products enter exactly; sums are fp32.  A
+ * scale multiplies the fp32 sums of a group's runs of 128 values (of a shorter
+ * group's values); with bf16 A and E2M1 weights it multiplies the weights,
+ * exactly.  So an infinite scale of a long group gives NaN if its runs' sums
+ * differ in sign or one is zero.  With bf16 A and U4 weights a run's sum is
+ * that of A w less z times that of A: a row of A holding an infinity, or values
+ * whose sums leave fp32's range, gives NaN.
  * Returns MSWZ_OK, MSWZ_ERR_INVALID or MSWZ_ERR_UNSUPPORTED.
  */
 int gemm_w4_plan_create(gemm_w4_plan **out, int64_t M, int64_t N, int64_t K, int64_t E, int a_dt,

@@ -7,7 +7,8 @@
 // bits) and multiplied against the activations with 16x16x32 MFMAs, for one
 // row as for sixteen: the MFMA takes 16 cycles per 512 weights, less than the
 // conversions, which a dot product on the vector unit would come on top of.
-// A scale multiplies the fp32 sum of its group, so no weight is rounded.
+// A scale multiplies fp32 sums of at most 128 values of its group, so no weight
+// is rounded.
 //
 // One workgroup of eight waves owns up to ROWS rows and 16*NB*NG columns of D.
 // Its waves split the columns NG ways and K KQ ways (NG * KQ = 8): a step is
@@ -361,8 +362,10 @@ w4_kernel(W4Kernel p)
     };
     // This lane's scales and zero points (absent ones are copied as zeros) of
     // column block nb, step t in the stage: spans 0 .. kSpans - 1 of the wave's
-    // chunk (folded scales: the lane group's own).  A scale behind the last one
-    // has no value of A either, but if it was not finite it would still count.
+    // chunk (folded scales: the lane group's own).  A span that starts at or
+    // behind K has no value of A, but its scale, the next row's or, in groups
+    // longer than a chunk, the last group's, would still count if it was not
+    // finite.
     const uint32_t no_z = p.Z ? 0u : 8u;
     const uint32_t s_col = uint32_t(n0 + 16 * NB * ng + r) * uint32_t(p.groups);   // first scale of block 0's column
     // bytes of block nb's first scale and zero point past a word, and their words' places
@@ -388,9 +391,11 @@ w4_kernel(W4Kernel p)
             for (int g = 0; g < kSpans; ++g)
                 zv[g] = *(st + z_at + 64 * kZWords * nb + g);
         }
+        // chunk c0 + kq's values from K on have a scale of zero
+        const int k0 = (c0 + kq) * kChunk - p.K;
 #pragma unroll
         for (int g = 0; g < kSpans; ++g)   // (no branch: it would cost the loop its registers)
-            sv[g] &= uint32_t((g1 + (kPre ? q : g) - p.groups) >> 31);
+            sv[g] &= uint32_t((k0 + (kPre ? 32 * q : SPAN * g)) >> 31);
     };
     // A step's LDS reads all come before the work on them (64 rows: one MFMA's
     // rows ahead), since two waves a SIMD cannot hide one read's latency after

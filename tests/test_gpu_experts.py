@@ -822,3 +822,25 @@ def test_w4_largest_e8m0_scales(M, a):
     assert torch.isinf(ref[odd]).all()
     assert torch.equal(got[odd].double(), ref[odd])
     check(got[~odd], ref[~odd], mag[~odd], K, "f32")
+
+
+@pytest.mark.parametrize("M,N,K,G", [(1, 16, 128, 1024), (3, 40, 32, 128), (16, 33, 160, 256), (20, 70, 160, 384), (64, 100, 8096, 8192),
+                                     (2, 70000, 96, 256)])
+@pytest.mark.parametrize("a", ["f16", "bf16"])
+def test_w4_scales_that_are_not_finite(M, N, K, G, a):
+    """An infinite scale gives an infinite sum and NaN a NaN in its own column only; the chunks of 128 values
+    that lie behind K add nothing."""
+    x = w4_inputs(gen(K + G), M, N, K, 0, a, "u4", G, True)
+    x["A"] = x["A"].abs() + 0.5            # sums of one sign
+    x["B"] |= 0x88                         # weights 8 .. 15
+    x["Z"] %= 8                            # zero points 0 .. 7
+    x["S"][0, ::5, -1] = float("inf")
+    x["S"][0, 1::5, 0] = -float("inf")
+    x["S"][0, 2::5, -1] = float("nan")
+    plan = mswz.gemm_w4_plan_create(M, N, K, a, "u4", "f32", group=G)
+    got = w4_run(plan, x, torch.zeros((M, N), device="cuda")).cpu()
+    assert (got[:, ::5] == float("inf")).all() and (got[:, 1::5] == -float("inf")).all() and torch.isnan(got[:, 2::5]).all()
+    x["S"][~torch.isfinite(x["S"])] = 0.0
+    ref, mag = w4_reference(x, "u4", G, a)
+    for i in (3, 4):
+        check(got[:, i::5], ref[:, i::5], mag[:, i::5], K, "f32")
