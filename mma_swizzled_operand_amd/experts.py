@@ -13,13 +13,14 @@ the plan's sizes and types and must share one GPU; a call runs on that GPU, on
 from __future__ import annotations
 
 import ctypes
+import functools
 
-import torch
+torch = None    # imported by the first call that takes tensors; the package and its plans work without it
 
 __all__ = ["W4Plan", "GroupedPlan", "MoePlan", "gemm_w4_plan_create", "gemm_run_w4", "gemm_grouped_plan_create",
            "gemm_run_grouped", "moe_plan_create", "moe_dispatch", "moe_combine", "moe_combine_grad"]
 
-_TORCH = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+_TORCH = {"f16": "float16", "bf16": "bfloat16", "f32": "float32"}
 _WEIGHTS = {"u4": 9, "e2m1": 5}
 _AXES = {"m": 0, "k": 1}
 
@@ -44,6 +45,25 @@ def declare(h):
             ("moe_combine_grad", [vp, vp, vp, vp, vp, vp, vp, vp], c_int)):
         f = getattr(h, name)
         f.argtypes, f.restype = args, res
+
+
+def _need_torch():
+    global torch, _current_stream
+    if torch is None:
+        import torch as module
+        # The handle of torch's current stream of a GPU.  (torch.cuda.current_stream
+        # makes a stream object first: 1.1 us of a call that takes 6.)
+        _current_stream = getattr(module._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: module.cuda.current_stream(dev).cuda_stream)
+        torch = module   # (last: another thread goes by it)
+
+
+def _type(name):
+    """torch's name of an element type, looked up when it is first asked for."""
+    def get(plan):
+        _need_torch()
+        return getattr(torch, _TORCH[getattr(plan, name)])
+    return functools.cached_property(get)
 
 
 class _Plan:
@@ -97,6 +117,12 @@ def _pick(table, name, what):
 class W4Plan(_Plan):
     """A product with 4-bit weights (gemm_w4_plan_create)."""
     _make, _free = "gemm_w4_plan_create", "gemm_w4_plan_destroy"
+    a_type, d_type = _type("a_dt"), _type("d_dt")
+
+    @functools.cached_property
+    def s_type(self):
+        _need_torch()
+        return self.a_type if self.w_dt == "u4" else torch.uint8
 
     def __init__(self, M, N, K, a_dt="bf16", w_dt="u4", d_dt="bf16", group=128, experts=0, lda=0, ldd=0):
         self.M, self.N, self.K, self.E = int(M), int(N), int(K), int(experts)
@@ -104,8 +130,6 @@ class W4Plan(_Plan):
                      int(group), int(lda), int(ldd))
         self.a_dt, self.w_dt, self.d_dt, self.group = a_dt, w_dt, d_dt, int(group)
         self.lda, self.ldd = int(lda) or self.K, int(ldd) or self.N
-        self.a_type, self.d_type = _TORCH[a_dt], _TORCH[d_dt]
-        self.s_type = self.a_type if w_dt == "u4" else torch.uint8
         matrices = max(1, self.E)
         self.b_numel = matrices * self.N * (self.K // 2)
         self.s_numel = matrices * self.N * (-(-self.K // self.group))
@@ -119,6 +143,7 @@ class W4Plan(_Plan):
 class GroupedPlan(_Plan):
     """A product over groups of rows (gemm_grouped_plan_create)."""
     _make, _free = "gemm_grouped_plan_create", "gemm_grouped_plan_destroy"
+    type, d_type = _type("dt"), _type("d_dt")
 
     def __init__(self, E, M, N, K, dt="bf16", d_dt="f32", axis="m", b_major=None):
         from . import MAJORS
@@ -127,7 +152,6 @@ class GroupedPlan(_Plan):
         self._create(self.E, self.M, self.N, self.K, _dt(dt), _dt(d_dt), _pick(_AXES, axis, "axis"),
                      _pick(MAJORS, b_major, "major"))
         self.dt, self.d_dt, self.axis, self.b_major = dt, d_dt, axis, b_major
-        self.type, self.d_type = _TORCH[dt], _TORCH[d_dt]
         self.a_numel = self.M * self.K
         self.b_numel = self.K * self.N * (1 if axis == "k" else self.E)
         self.d_numel = self.M * self.N * (self.E if axis == "k" else 1)
@@ -137,11 +161,12 @@ class GroupedPlan(_Plan):
 class MoePlan(_Plan):
     """The token movement of T tokens of H elements and topk choices among E experts (moe_plan_create)."""
     _make, _free = "moe_plan_create", "moe_plan_destroy"
+    type = _type("dt")
 
     def __init__(self, T, topk, E, H, dt="bf16", ldx=0):
         self.T, self.topk, self.E, self.H = int(T), int(topk), int(E), int(H)
         self._create(self.T, self.topk, self.E, self.H, _dt(dt), int(ldx))
-        self.dt, self.ldx, self.type = dt, int(ldx) or self.H, _TORCH[dt]
+        self.dt, self.ldx = dt, int(ldx) or self.H
         self.choices = self.T * self.topk
         self.ws_bytes = int(self._lib.moe_plan_workspace_size(self._h))
         self._dispatch, self._combine = self._lib.moe_dispatch, self._lib.moe_combine
@@ -206,18 +231,14 @@ def _device(plan, kind, t, name):
         raise TypeError(f"expected a {kind.__name__}, got {type(plan).__name__}")
     if plan._h is None:
         raise ValueError("plan has been destroyed")
+    if torch is None:
+        _need_torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name}: tensor must live in GPU memory")
     return dev
-
-
-# The handle of torch's current stream of a GPU.  (torch.cuda.current_stream
-# makes a stream object first: 1.1 us of a call that takes 6.)
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _call(fn, what, dev, stream, *args):

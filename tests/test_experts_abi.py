@@ -5,6 +5,8 @@ values are enough to reach the checks)."""
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -235,3 +237,28 @@ def test_numbers_wider_than_the_argument_are_refused(make):
     for wide in (1, -1):
         with pytest.raises(mswz.MswzError):
             make(wide)
+
+
+def test_package_and_plans_work_without_torch():
+    """torch supplies memory and streams to the run calls; nothing before them asks for it."""
+    code = """
+import sys
+sys.modules["torch"] = None    # importing it raises
+import mma_swizzled_operand_amd as mswz
+assert mswz.tile_offset(3, 1) >= 0 and mswz.desc_check(16, 1024, 2) is not None
+assert mswz.gemm_plan_create(256, 256, 64, "bf16", "bf16").describe()["tile_m"] > 0
+assert mswz.gemm_w4_plan_create(64, 300, 8192).workspace_bytes() > 0
+assert mswz.gemm_grouped_plan_create(2, 64, 64, 64).d_numel == 64 * 64
+assert mswz.moe_plan_create(5000, 2, 8, 64).workspace_bytes() > 0
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def test_types_of_a_plan():
+    w4 = mswz.gemm_w4_plan_create(1, 16, 64, "f16", "u4", "f32", group=64)
+    assert (w4.a_type, w4.s_type, w4.d_type) == (torch.float16, torch.float16, torch.float32)
+    assert mswz.gemm_w4_plan_create(1, 16, 64, "bf16", "e2m1", "bf16", group=32).s_type is torch.uint8
+    grouped = mswz.gemm_grouped_plan_create(2, 64, 64, 64, "bf16", "f32")
+    assert (grouped.type, grouped.d_type) == (torch.bfloat16, torch.float32)
+    assert mswz.moe_plan_create(1, 1, 1, 8, "f16").type is torch.float16
