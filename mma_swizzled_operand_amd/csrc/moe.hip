@@ -21,7 +21,8 @@ constexpr int kRounds = 4;                                  // choices per lane
 constexpr int kSlots = kSortThreads * kRounds;              // choices per workgroup of the sort
 constexpr int kMaxE = 1024;
 constexpr int kFew = 1024;                                  // choices that one launch sorts and copies
-constexpr int kUncounted = 8192;                            // choices that each workgroup of the sort counts itself
+constexpr int kUncountedMost = 8192;                        // choices that each workgroup of the sort counts itself
+constexpr int kCountedMost = 16384, kCountedGroups = 256;   // counts, of so many workgroups, that each one adds up itself
 
 // Lanes that hold the same key, as a mask: one ballot per key bit.
 __device__ __forceinline__ uint64_t same_key(uint32_t key, int bits)
@@ -83,15 +84,69 @@ moe_count_kernel(const int32_t *__restrict__ ids, int n, int E, int32_t *__restr
         counts[int64_t(blockIdx.x) * E + e] = hist[e];
 }
 
+// Each expert's counts of the workgroups, in place, become what the workgroups
+// before it hold, and row `groups` the expert's total.  A workgroup takes
+// `width` experts (a power of two); its threads of one expert take a run of
+// rows each: one pass adds up the run, a scan over the runs gives each its
+// start, a second pass writes.  Eight loads in flight, as in the sort.
+constexpr int kScanThreads = 1024, kScanWidth = 16;
+__global__ void __launch_bounds__(kScanThreads)
+moe_scan_kernel(int32_t *__restrict__ counts, int groups, int E, int width)
+{
+    __shared__ int32_t sums[kScanThreads];
+    const int tid = threadIdx.x, parts = kScanThreads / width, part = tid / width, e = blockIdx.x * width + tid % width;
+    const int run = (groups + parts - 1) / parts, g0 = min(part * run, groups), g1 = min(g0 + run, groups);
+    int32_t *const c = counts + min(e, E - 1);
+    int sum = 0;
+    for (int g = g0; g < g1; g += 8) {
+        int v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = c[int64_t(min(g + i, g1 - 1)) * E];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            sum += g + i < g1 ? v[i] : 0;
+    }
+    // (runs of one expert lie `width` apart)
+    sums[tid] = sum;
+    __syncthreads();
+    for (int d = width; d < kScanThreads; d *= 2) {
+        const int before = tid >= d ? sums[tid - d] : 0;
+        __syncthreads();
+        sums[tid] += before;
+        __syncthreads();
+    }
+    if (e >= E)
+        return;
+    int before = sums[tid] - sum;
+    for (int g = g0; g < g1; g += 8) {
+        int v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = c[int64_t(min(g + i, g1 - 1)) * E];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (g + i < g1) {
+                c[int64_t(g + i) * E] = before;
+                before += v[i];
+            }
+    }
+    if (part == parts - 1)
+        c[int64_t(groups) * E] = before;
+}
+
 // Places of a workgroup's choices: the counts of all workgroups give each
 // expert's first row and what earlier workgroups put before this one's
-// choices, the waves' own counts the rest.  With COUNTS each workgroup adds up
+// choices, the waves' own counts the rest.  kCounted: each workgroup adds up
 // moe_count_kernel's counts (from L2), several threads an expert, eight loads
-// of each in flight: one load at a time took 20 us at 32 workgroups.  Without,
-// it counts all choices itself, which saves the other kernel's launch while
-// there are few: sort and copy of 2048 / 8192 / 16384 choices with it 10.5 /
-// 12.4 / 15.1 us, without 8.4 / 11.7 / 16.8.
-template <bool COUNTS>
+// of each in flight: one load at a time took 20 us at 32 workgroups.
+// kUncounted: it counts all choices itself, which saves the other kernel's
+// launch while there are few: sort and copy of 2048 / 8192 / 16384 choices with
+// it 10.5 / 12.4 / 15.1 us, without 8.4 / 11.7 / 16.8.  kScanned: it finds its
+// sums in moe_scan_kernel's table, since adding up all counts in every
+// workgroup grows with the square of the choices.
+enum Sort { kUncounted, kCounted, kScanned };
+template <Sort SORT>
 __global__ void __launch_bounds__(kSortThreads)
 moe_place_kernel(const int32_t *__restrict__ ids, int n, int E, int bits, const int32_t *__restrict__ counts,
                  int32_t *__restrict__ offsets, int32_t *__restrict__ order, int32_t *__restrict__ pos)
@@ -106,7 +161,12 @@ moe_place_kernel(const int32_t *__restrict__ ids, int n, int E, int bits, const 
             hist[w][e] = 0;
     }
     __syncthreads();
-    if constexpr (COUNTS) {
+    if constexpr (SORT == kScanned) {
+        for (int e = tid; e < E; e += kSortThreads) {
+            total[e] = counts[int64_t(groups) * E + e];
+            base[e] = counts[int64_t(blockIdx.x) * E + e];
+        }
+    } else if constexpr (SORT == kCounted) {
         // experts in columns of `width` threads, groups dealt to the rows of threads
         int width = 64;
         while (width < E && width < kSortThreads)
@@ -492,10 +552,25 @@ int bits_for(int E)
 
 static bool few(const MoeArgs &a) { return a.T * a.topk <= kFew; }
 
+static int64_t sort_groups(const MoeArgs &a) { return (int64_t(a.T) * a.topk + kSlots - 1) / kSlots; }
+
+// How the sort finds its sums.  The scan costs a launch and saves every
+// workgroup the reading of all counts; the sort alone in a graph, counted /
+// scanned, in us: 16 workgroups and 1024 experts 14.2 / 14.8, 32: 18.2 / 15.1;
+// 128 and 128 12.9 / 14.0, 256: 16.8 / 14.6; 256 and 64 13.1 / 14.1, 512: 17.8
+// / 15.7; 256 and 8 13.5 / 13.3, 512: 17.0 / 14.1; 1024 and 1024 414 / 30.
+static Sort sort_of(const MoeArgs &a)
+{
+    const int64_t groups = sort_groups(a);
+    if (int64_t(a.T) * a.topk <= kUncountedMost)
+        return kUncounted;
+    return groups <= kCountedGroups && groups * a.E <= kCountedMost ? kCounted : kScanned;
+}
+
 int64_t moe_workspace_bytes(const MoeArgs &a)
 {
-    const int64_t n = int64_t(a.T) * a.topk;
-    return n <= kUncounted ? 0 : (n + kSlots - 1) / kSlots * a.E * 4;
+    const Sort sort = sort_of(a);
+    return sort == kUncounted ? 0 : (sort_groups(a) + (sort == kScanned)) * a.E * 4;
 }
 
 hipError_t launch_moe_dispatch(const MoeArgs &a, const int32_t *ids, const void *X, void *Xs, int32_t *offsets,
@@ -507,15 +582,27 @@ hipError_t launch_moe_dispatch(const MoeArgs &a, const int32_t *ids, const void 
                            offsets, order, pos);
         return hipGetLastError();
     }
-    const int n = a.T * a.topk, groups = (n + kSlots - 1) / kSlots;
-    if (n <= kUncounted) {
-        hipLaunchKernelGGL(moe_place_kernel<false>, dim3(groups), dim3(kSortThreads), 0, stream, ids, n, a.E,
-                           bits_for(a.E), static_cast<const int32_t *>(nullptr), offsets, order, pos);
+    const int n = a.T * a.topk, groups = int(sort_groups(a));
+    const int bits = bits_for(a.E);
+    int32_t *counts = static_cast<int32_t *>(workspace);
+    const Sort sort = sort_of(a);
+    if (sort == kUncounted) {
+        hipLaunchKernelGGL(moe_place_kernel<kUncounted>, dim3(groups), dim3(kSortThreads), 0, stream, ids, n, a.E, bits,
+                           static_cast<const int32_t *>(nullptr), offsets, order, pos);
     } else {
-        int32_t *counts = static_cast<int32_t *>(workspace);
         hipLaunchKernelGGL(moe_count_kernel, dim3(groups), dim3(kSortThreads), 0, stream, ids, n, a.E, counts);
-        hipLaunchKernelGGL(moe_place_kernel<true>, dim3(groups), dim3(kSortThreads), 0, stream, ids, n, a.E, bits_for(a.E),
-                           counts, offsets, order, pos);
+        if (sort == kCounted) {
+            hipLaunchKernelGGL(moe_place_kernel<kCounted>, dim3(groups), dim3(kSortThreads), 0, stream, ids, n, a.E, bits,
+                               counts, offsets, order, pos);
+        } else {
+            int width = 1;
+            while (width < kScanWidth && width < a.E)
+                width *= 2;
+            hipLaunchKernelGGL(moe_scan_kernel, dim3((a.E + width - 1) / width), dim3(kScanThreads), 0, stream, counts, groups,
+                               a.E, width);
+            hipLaunchKernelGGL(moe_place_kernel<kScanned>, dim3(groups), dim3(kSortThreads), 0, stream, ids, n, a.E, bits,
+                               counts, offsets, order, pos);
+        }
     }
     if (X) {
         const int lg = waves_log2(a);

@@ -844,3 +844,76 @@ def test_w4_scales_that_are_not_finite(M, N, K, G, a):
     ref, mag = w4_reference(x, "u4", G, a)
     for i in (3, 4):
         check(got[:, i::5], ref[:, i::5], mag[:, i::5], K, "f32")
+
+
+@pytest.mark.parametrize("T,topk,E", [
+    (16 * 1024, 1, 1024), (16 * 1024 + 1, 1, 1024),          # the edges between the ways of adding up counts
+    (128 * 1024, 1, 128), (128 * 1024, 1, 129), (256 * 1024, 1, 3), (256 * 1024 + 1, 1, 3),
+    (40000, 7, 1), (70001, 5, 17), (90000, 8, 300), (1 << 21, 2, 1000), ((1 << 24) - 1, 1, 1024), ((1 << 21) - 1, 8, 2),
+])
+def test_sort_of_many_choices(T, topk, E):
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    ids = torch.randint(-1, E + 1, (T, topk), generator=g, device="cuda", dtype=torch.int32)
+    plan, n = mswz.moe_plan_create(T, topk, E, 8, "bf16"), T * topk
+    key = torch.where((ids < 0) | (ids >= E), E, ids).reshape(-1)
+    key, slot = torch.sort(key, stable=True)
+    offsets = torch.searchsorted(key, torch.arange(E + 1, device="cuda", dtype=torch.int32)).to(torch.int32)
+    order = torch.where(key < E, slot, -1).to(torch.int32)
+    pos = torch.empty_like(order)
+    pos[slot] = torch.where(key < E, torch.arange(n, device="cuda"), -1).to(torch.int32)
+    need = plan.workspace_bytes()
+    out = [torch.full((m,), -99, dtype=torch.int32, device="cuda") for m in (E + 1, n, n)]
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    mswz.moe_dispatch(plan, ids, None, None, *out, workspace=ws[:need])
+    for got, want in zip(out, (offsets, order, pos)):
+        assert torch.equal(got, want)
+    assert (ws[need:] == 0xFF).all()
+
+
+def test_sort_of_many_choices_captured_and_replayed():
+    T, topk, E, H = 50000, 8, 200, 16
+    plan, n = mswz.moe_plan_create(T, topk, E, H, "f16"), T * topk
+    ids, X = torch.zeros(T, topk, dtype=torch.int32, device="cuda"), torch.zeros(T, H, dtype=torch.float16, device="cuda")
+    i32 = lambda m: torch.zeros(m, dtype=torch.int32, device="cuda")
+    out, Xs = [i32(E + 1), i32(n), i32(n)], torch.zeros(n, H, dtype=torch.float16, device="cuda")
+    ws = torch.empty(plan.workspace_bytes(), dtype=torch.uint8, device="cuda")
+    mswz.moe_dispatch(plan, ids, X, Xs, *out, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mswz.moe_dispatch(plan, ids, X, Xs, *out, workspace=ws)
+    for seed in (80, 81, 82):
+        g = gen(seed)
+        new, rows = ids_for(g, T, topk, E, 0.1), normal(g, T, H, dt="f16")
+        ids.copy_(new)
+        X.copy_(rows)
+        Xs.fill_(GUARD)
+        ws.fill_(0xFF)
+        torch.cuda.synchronize()
+        graph.replay()
+        want = dispatch(plan, new, X)
+        assert all(torch.equal(a, b.reshape(-1)) for a, b in zip(out, want))
+        assert torch.equal(Xs, want[3])
+        ref = sorted_reference(new, E)
+        assert all(np.array_equal(a.cpu().numpy(), b.reshape(-1)) for a, b in zip(out, ref))
+
+
+def test_sort_does_not_grow_with_the_square_of_the_choices():
+    """Four times the choices take at most eight times as long (they took 12.8 times with every workgroup adding up
+    the counts of all others)."""
+    E, times = 1024, []
+    for T in (1 << 17, 1 << 19):
+        plan, n = mswz.moe_plan_create(T, 8, E, 8, "bf16"), T * 8
+        ids = torch.randint(0, E, (T, 8), device="cuda", dtype=torch.int32)
+        out = [torch.zeros(m, dtype=torch.int32, device="cuda") for m in (E + 1, n, n)]
+        ws = torch.empty(plan.workspace_bytes(), dtype=torch.uint8, device="cuda")
+        best = float("inf")
+        for _ in range(8):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            mswz.moe_dispatch(plan, ids, None, None, *out, workspace=ws)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        times.append(best)
+    assert times[1] <= 8 * times[0], times
