@@ -217,20 +217,15 @@ w4_kernel(W4Kernel p)
     constexpr int kSCopies = (kCols * kSWords + kSThreads - 1) / kSThreads;
     constexpr int kSBytes = kSCopies * kSThreads * 4;         // (whole copies: what lies behind is not read)
     constexpr int kStageBytes = kABytes + (E2M1 ? 1 : 2) * kSBytes;
-    // one named array per stage: the compiler then knows which stage a copy
-    // writes, and waits for no other one
     // LDS stages and register slots; steps in flight.  (Three stages leave room
     // for a second or third workgroup: one row by 16384 x 8192 with two, three,
     // four: 18.4, 14.1, 14.6 us)
     constexpr int kStages = STAGES, kAhead = STAGES - 1;
-    static_assert(STAGES >= 2 && STAGES <= 8, "named stages");
-#define W4_STAGE(i) \
-    __shared__ __attribute__((aligned(1024))) uint8_t st##i[i < STAGES ? kStageBytes : 4];
-    W4_STAGE(0) W4_STAGE(1) W4_STAGE(2) W4_STAGE(3) W4_STAGE(4) W4_STAGE(5) W4_STAGE(6) W4_STAGE(7)
-#undef W4_STAGE
-    auto stage = [&](int u) {
-        return u == 0 ? st0 : u == 1 ? st1 : u == 2 ? st2 : u == 3 ? st3 : u == 4 ? st4 : u == 5 ? st5 : u == 6 ? st6 : st7;
-    };
+    static_assert(STAGES == 2 || STAGES == 3, "named stages");
+    // one named array per stage: the compiler then knows which stage a copy
+    // writes, and waits for no other one
+    __shared__ __attribute__((aligned(1024))) uint8_t st0[kStageBytes], st1[kStageBytes], st2[STAGES == 3 ? kStageBytes : 4];
+    auto stage = [&](int u) { return u == 0 ? st0 : u == 1 ? st1 : st2; };
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, q = lane >> 4, ng = wave % NG, kq = wave / NG;
@@ -629,7 +624,6 @@ hipError_t launch_w4_tile(const W4Args &a, hipStream_t stream)
     return hipGetLastError();
 }
 
-#ifndef W4_TUNE
 // Columns of a workgroup: as many as leave a workgroup for every compute unit
 // (two, for the longest), since more columns share a copy of A and a step's
 // addresses, and make a wave's part of K and with it its run of steps longer.
@@ -662,7 +656,6 @@ hipError_t launch_w4_span(const W4Args &a, hipStream_t stream)
                                                             : launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 2, 2>(a, stream);
     return rows == 16 ? launch_w4_cols<BF16, E2M1, SPAN, 16>(a, stream) : launch_w4_cols<BF16, E2M1, SPAN, 4>(a, stream);
 }
-#endif
 
 template <bool BF16, bool E2M1>
 hipError_t launch_w4_kind(const W4Args &a, hipStream_t stream)
