@@ -917,3 +917,71 @@ def test_sort_does_not_grow_with_the_square_of_the_choices():
             best = min(best, a.elapsed_time(b))
         times.append(best)
     assert times[1] <= 8 * times[0], times
+
+
+W4_FORMS = [  # rows an expert, experts, N, steps' K: the widths and stages that the sizes choose (gemm_w4_kernel.hpp)
+    (2, 64, 1000, 256), (3, 32, 510, 512), (4, 33, 250, 512), (2, 5, 100, 1024),           # tiles of 4 rows
+    (7, 64, 1000, 256), (16, 32, 510, 512), (9, 17, 286, 512), (5, 4, 100, 1024),          # of 16
+    (17, 64, 510, 256), (40, 5, 130, 512),                                                 # of 64
+]
+
+
+def w4_large_inputs(seed, M, N, K, E, a, w, G):
+    """w4_inputs, made on the GPU."""
+    g, x, sh = torch.Generator(device="cuda").manual_seed(seed), {"Z": None}, (max(1, E), N, -(-K // G))
+    x["A"] = torch.randn(M, K, generator=g, device="cuda").to(DT[a])
+    x["B"] = torch.randint(0, 256, (sh[0], N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    if w == "u4":
+        x["S"] = ((0.5 + torch.rand(sh, generator=g, device="cuda")) * 0.02).to(DT[a])
+        x["Z"] = torch.randint(0, 16, sh, generator=g, device="cuda", dtype=torch.uint8)
+    else:
+        x["S"] = torch.randint(118, 130, sh, generator=g, device="cuda", dtype=torch.uint8)
+    return x
+
+
+def w4_columns(x, cols):
+    """The inputs of some columns of D, on the CPU."""
+    return {k: v if v is None else (v if k == "A" else v[:, cols.cuda()]).cpu() for k, v in x.items()}
+
+
+@pytest.mark.parametrize("steps", [2.6, 4, 5.2, 7, 8.5, 9])
+@pytest.mark.parametrize("a,w,G", [("f16", "u4", 32), ("bf16", "u4", 64), ("f16", "u4", 128), ("bf16", "u4", 384),
+                                   ("bf16", "e2m1", 32), ("f16", "e2m1", 32)])
+def test_w4_many_steps(a, w, G, steps):
+    """Every form of the kernel over whole and partial rounds of its stages, the last step whole and partly filled."""
+    for rows, E, N, step in W4_FORMS:
+        K = int(steps * step) // 32 * 32
+        M, cols = rows * E, torch.cat((torch.arange(0, N - 16, 9), torch.arange(N - 16, N)))
+        counts = torch.randint(0, 2 * rows + 1, (E,), generator=gen(K + E))
+        while int(counts.sum()) > M:
+            counts[int(counts.argmax())] //= 2
+        bounds = bounds_of(counts.tolist())
+        x = w4_large_inputs(K + E, M, N, K, E, a, w, G)
+        plan = mswz.gemm_w4_plan_create(M, N, K, a, w, "f32", group=G, experts=E)
+        assert plan.workspace_bytes() == 0
+        got = w4_run(plan, x, torch.full((M, N), GUARD, device="cuda"), bounds.cuda())
+        used = int(bounds[-1])
+        ref, mag = w4_reference(w4_columns(x, cols), w, G, a, bounds.tolist())
+        check(got[:used][:, cols.cuda()], ref[:used], mag[:used], K, "f32", (rows, E, N, K))
+        assert torch.isfinite(got).all() and (got[used:] == GUARD).all()
+        again = w4_run(plan, x, torch.full((M, N), GUARD, device="cuda"), bounds.cuda())
+        assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("M,N,K,G,a,w,d", [
+    (64, 16400, 4640, 32, "bf16", "e2m1", "bf16"), (50, 16400, 4640, 64, "bf16", "u4", "bf16"),
+    (64, 16390, 2560, 128, "f16", "u4", "f32"), (64, 32900, 1120, 32, "bf16", "e2m1", "f32"),
+    (33, 32800, 1536, 32, "f16", "e2m1", "f32"), (130, 16400, 1312, 128, "bf16", "u4", "f32"),
+    (64, 700, 8224, 32, "bf16", "e2m1", "bf16"), (20, 260, 12320, 64, "bf16", "u4", "f32"),
+])
+def test_w4_one_matrix_many_steps(M, N, K, G, a, w, d):
+    """17 rows and more by one matrix: two and three stages, K whole and split over workgroups."""
+    cols = torch.cat((torch.arange(0, N - 70, 23), torch.arange(N - 70, N)))
+    x = w4_large_inputs(K + N, M, N, K, 0, a, w, G)
+    plan = mswz.gemm_w4_plan_create(M, N, K, a, w, d, group=G)
+    got = w4_run(plan, x, torch.full((M, N), float("nan"), dtype=DT[d], device="cuda"))
+    ref, mag = w4_reference(w4_columns(x, cols), w, G, a)
+    check(got[:, cols.cuda()], ref, mag, K, d)
+    assert torch.isfinite(got).all()
+    again = w4_run(plan, x, torch.zeros((M, N), dtype=DT[d], device="cuda"))
+    assert torch.equal(got, again)
