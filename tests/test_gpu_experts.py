@@ -985,3 +985,155 @@ def test_w4_one_matrix_many_steps(M, N, K, G, a, w, d):
     assert torch.isfinite(got).all()
     again = w4_run(plan, x, torch.zeros((M, N), dtype=DT[d], device="cuda"))
     assert torch.equal(got, again)
+
+
+# ---- calls that the header allows ----------------------------------------------------------
+
+@pytest.mark.parametrize("T,topk,E,H,ld,dt", [(1, 1024, 30, 16, 0, "f16"), (3, 300, 1024, 4200, 4304, "bf16"), (9, 2, 4, 8200, 0, "f32"),
+                                              (700, 2, 9, 72, 96, "f16"), (300, 5, 6, 4200, 4304, "bf16"), (9000, 1, 6, 520, 528, "f32")])
+def test_dispatch_of_wide_and_pitched_rows(T, topk, E, H, ld, dt):
+    g = gen(T + H)
+    ids, X = ids_for(g, T, topk, E, 0.1), normal(g, T, H, dt=dt)
+    plan = mswz.moe_plan_create(T, topk, E, H, dt, ldx=ld)
+    wide = torch.full((T, ld or H), float("nan"), dtype=DT[dt], device="cuda")
+    wide[:, :H] = X.cuda()
+    offsets, order, pos, Xs = dispatch(plan, ids, wide[:, :H])
+    want = sorted_reference(ids, E)
+    assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip((offsets, order, pos), want))
+    used = int(want[0][-1])
+    assert torch.equal(Xs[:used].cpu(), X[torch.from_numpy(want[1][:used].astype(np.int64) // topk)])
+    assert (Xs[used:] == GUARD).all()
+
+
+@pytest.mark.parametrize("T,topk,H,dt", [(40, 3, 72, "bf16"), (700, 9, 264, "f32")])
+def test_combine_of_any_positions(T, topk, H, dt):
+    """A row named twice counts twice; positions outside the rows add nothing and leave dYs as it was."""
+    g, n = gen(T + 90), T * topk
+    Ys, dY, w = normal(g, n, H, dt=dt), normal(g, T, H, dt=dt), torch.randn(T, topk, generator=g)
+    plan = mswz.moe_plan_create(T, topk, 4, H, dt)
+    wrong = torch.tensor([-1, n, n + 1, -(1 << 31), (1 << 31) - 1])
+    pos = torch.randint(0, n, (T, topk), generator=g)
+    out = torch.rand(T, topk, generator=g) < 0.2
+    pos[out] = wrong[torch.randint(0, 5, (int(out.sum()),), generator=g)]
+    w[out] = float("inf")
+    rows, wk = Ys[pos.clamp(0, n - 1)].double(), torch.where(out, 0.0, w).double()
+    Y = torch.full((T, H), float("nan"), dtype=DT[dt], device="cuda")
+    mswz.moe_combine(plan, Ys.cuda(), pos.int().cuda(), Y, weights=w.cuda())
+    check(Y, (rows * wk[:, :, None]).sum(1), (rows * wk[:, :, None]).abs().sum(1), topk, dt)
+    pos = torch.randperm(n, generator=g).reshape(T, topk)   # each row once, in any order
+    pos[out] = wrong[torch.randint(0, 5, (int(out.sum()),), generator=g)]
+    dYs = torch.full((n, H), GUARD, dtype=DT[dt], device="cuda")
+    dw = torch.full((T, topk), float("nan"), device="cuda")
+    mswz.moe_combine_grad(plan, dY.cuda(), Ys.cuda(), pos.int().cuda(), w.cuda(), dYs, dw)
+    terms = torch.where(out[:, :, None], 0.0, Ys[pos.clamp(0, n - 1)].double() * dY.double()[:, None, :])
+    check(dw, terms.sum(2), terms.abs().sum(2), H, "f32")
+    want = torch.full((n, H), GUARD, dtype=DT[dt])
+    want[pos[~out]] = (w[:, :, None] * dY.float()[:, None, :]).to(DT[dt])[~out]
+    assert torch.equal(dYs.cpu(), want)
+
+
+def test_most_tokens():
+    """2^24 - 1 tokens through every call of the token movement."""
+    T, E, H = (1 << 24) - 1, 5, 8
+    plan, g = mswz.moe_plan_create(T, 1, E, H, "f16"), torch.Generator(device="cuda").manual_seed(91)
+    ids = torch.randint(0, E, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+    X = torch.randint(-8, 9, (T, H), generator=g, device="cuda").half()
+    offsets, order, pos, Xs = dispatch(plan, ids, X)
+    assert torch.equal(Xs, X[order.long()]) and torch.equal(order[pos[:, 0].long()].long(), torch.arange(T, device="cuda"))
+    w = torch.full((T, 1), 2.0, device="cuda")
+    Y, dYs, dw = torch.full_like(X, GUARD), torch.full_like(X, GUARD), torch.full_like(w, GUARD)
+    mswz.moe_combine(plan, Xs, pos, Y, weights=w)
+    assert torch.equal(Y, 2 * X)
+    mswz.moe_combine_grad(plan, X, Xs, pos, w, dYs, dw)
+    assert torch.equal(dYs, 2 * Xs) and torch.equal(dw[:, 0], (X.float() ** 2).sum(1))
+
+
+@pytest.mark.parametrize("a,w,G,per", [("f16", "u4", 64, 3), ("bf16", "u4", 128, 12), ("bf16", "e2m1", 32, 30), ("f16", "e2m1", 32, 2)])
+def test_w4_experts_with_pitches_beta_and_unaligned_d(a, w, G, per):
+    E, N, K, lda, ldd = 6, 45, 352, 368, 47
+    counts = [per, 0, 2 * per, 1, per - 1, 2 * per - 2]
+    M, g = 6 * per + 3, gen(per)
+    first = 2                              # rows before the first group and behind the last are left alone
+    bounds = bounds_of(counts) + first
+    x = w4_inputs(g, M, N, K, E, a, w, G, True)
+    ref, mag = w4_reference(x, w, G, a, bounds.tolist())
+    wide = torch.full((M, lda), float("nan"), dtype=DT[a])
+    wide[first:int(bounds[-1]), :K] = x["A"][first:int(bounds[-1])]
+    D0 = normal(g, M, ldd, dt=a)
+    room = torch.zeros(M * ldd + 1, dtype=DT[a], device="cuda")
+    D = room[1:].reshape(M, ldd)           # 2 bytes past a 16-byte boundary
+    D.copy_(D0)
+    plan = mswz.gemm_w4_plan_create(M, N, K, a, w, a, group=G, experts=E, lda=lda, ldd=ldd)
+    c = {k: None if v is None else v.cuda() for k, v in x.items()}
+    mswz.gemm_run_w4(plan, wide.cuda()[:, :K], c["B"], c["S"], D[:, :N], Z=c["Z"], offsets=bounds.cuda(), beta=1)
+    used = slice(first, int(bounds[-1]))
+    check(D[used, :N], (ref + D0[:, :N].double())[used], (mag + D0[:, :N].double().abs())[used], K, a)
+    D = D.cpu()
+    assert torch.equal(D[:, N:], D0[:, N:]) and torch.equal(D[:first], D0[:first]) and torch.equal(D[used.stop:], D0[used.stop:])
+
+
+@pytest.mark.parametrize("E", [0, 1024])
+def test_w4_most_rows(E):
+    M, N, K = 1 << 16, 24, 64
+    x = w4_large_inputs(92, M, N, K, E, "f16", "u4", 32)
+    bounds = None
+    if E:
+        cuts = torch.randint(0, M + 1, (E - 1,), generator=gen(93)).sort()[0]
+        bounds = torch.cat((torch.zeros(1), cuts, torch.full((1,), M))).int()
+    plan = mswz.gemm_w4_plan_create(M, N, K, "f16", "u4", "f32", group=32, experts=E)
+    got = w4_run(plan, x, torch.full((M, N), float("nan"), device="cuda"), bounds)
+    ref, mag = w4_reference(w4_columns(x, torch.arange(N)), "u4", 32, "f16", None if bounds is None else bounds.tolist())
+    check(got, ref, mag, K, "f32")
+
+
+def test_w4_split_captured_and_replayed():
+    """The product whose K is split over workgroups, with its workspace, as a graph."""
+    M, N, K = 40, 300, 8192
+    plan = mswz.gemm_w4_plan_create(M, N, K, "bf16", "u4", "bf16", group=128)
+    x = {k: torch.empty_like(v) for k, v in w4_large_inputs(94, M, N, K, 0, "bf16", "u4", 128).items()}
+    D, ws = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda"), torch.empty(plan.workspace_bytes(), dtype=torch.uint8, device="cuda")
+    run = lambda: mswz.gemm_run_w4(plan, x["A"], x["B"], x["S"], D, Z=x["Z"], workspace=ws)
+    assert plan.workspace_bytes() > 0
+    new = w4_large_inputs(95, M, N, K, 0, "bf16", "u4", 128)
+    for k in x:
+        x[k].copy_(new[k])
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for seed in (96, 97, 98):
+        new = w4_large_inputs(seed, M, N, K, 0, "bf16", "u4", 128)
+        for k in x:
+            x[k].copy_(new[k])
+        D.fill_(float("nan"))
+        ws.fill_(0xFF)
+        torch.cuda.synchronize()
+        graph.replay()
+        eager = w4_run(plan, new, torch.zeros_like(D))
+        assert torch.equal(D, eager)
+        check(D, *w4_reference(w4_columns(new, torch.arange(N)), "u4", 128, "bf16"), K, "bf16")
+
+
+@pytest.mark.parametrize("first,gap", [(1, 0), (70, 0), (5, 9)])
+def test_grouped_rows_before_the_first_group(first, gap):
+    """Bounds may start behind row 0: rows before the first group are neither read nor written."""
+    g, E, N, K, counts = gen(first), 3, 40, 136, [30, 0, 300]
+    rows = first + sum(counts) + gap
+    bounds = bounds_of(counts) + first
+    used = slice(first, first + sum(counts))
+    A, B = torch.full((rows, K), float("nan"), dtype=torch.bfloat16), normal(g, E, N, K)
+    A[used] = normal(g, sum(counts), K)
+    ref, mag = grouped_reference(A, B, bounds.tolist())
+    for b_major, stored in (("k", B), ("mn", B.transpose(1, 2).contiguous())):
+        D = torch.full((rows, N), GUARD, device="cuda")
+        mswz.gemm_run_grouped(mswz.gemm_grouped_plan_create(E, rows, N, K, b_major=b_major), A.cuda(), stored.cuda(), bounds.cuda(), D)
+        check(D[used], ref[used], mag[used], K, "f32")
+        assert (D[:first] == GUARD).all() and (D[used.stop:] == GUARD).all()
+    dY = torch.full((rows, N), float("inf"), dtype=torch.bfloat16)
+    dY[used] = normal(g, sum(counts), N)
+    dW = torch.full((E, N, K), float("nan"), device="cuda")
+    mswz.gemm_run_grouped(mswz.gemm_grouped_plan_create(E, N, K, rows, axis="k"), dY.cuda(), A.cuda(), bounds.cuda(), dW)
+    b = bounds.tolist()
+    parts = [(dY[b[e]:b[e + 1]].double(), A[b[e]:b[e + 1]].double()) for e in range(E)]
+    check(dW, torch.stack([y.t() @ a for y, a in parts]), torch.stack([y.abs().t() @ a.abs() for y, a in parts]), max(counts), "f32")
