@@ -42,21 +42,24 @@ int w4_rows(const W4Args &a)
 {
     // rows that a tile is expected to hold: experts share them (16384 x 8192, u4:
     // one row in tiles of 4 takes 13.5 us, 16 in tiles of 16 15.9, 64 in tiles
-    // of 64 30)
+    // of 64 31.4).  An expert with more has more tiles, whose weights come from
+    // the L2: 128 rows and 32 experts of 4096 x 2048 take 46 us spread evenly,
+    // 27 if all of them go to one expert.
     const int64_t rows = a.E ? (int64_t(a.M) + a.E - 1) / a.E : a.M;
     return rows > 16 ? 64 : rows > 4 ? 16 : 4;
 }
 
 int64_t w4_tiles64(const W4Args &a) { return a.E ? (a.E < a.M ? a.E : a.M) : (a.M + 63) / 64; }
 
-// K parts of a product: where tiles of 64 rows by 64 columns leave compute
-// units idle, K is split between those of 64 x 128 until there are as many,
-// each part keeping at least four steps of 256.  (64 rows by 16384 x 8192, when
-// tiles of 128 columns were the only ones: 52 us unsplit, 32 and 4.9 for the sum
-// in two parts.)
+// K parts of a product: where tiles of 64 rows by 64 columns leave half of the
+// compute units idle, K is split between those of 64 x 128 until there are as
+// many, each part keeping at least four steps of 256.  (64 rows by K 8192, 64
+// columns unsplit / split and added up: N 4096, U4 29.8 / 17.8 us, 8192: 30.7 /
+// 23.3, 10240: 30.7 / 37.3, 14336: 31.3 / 40.2; FP4 23.9 / 15.9, 23.8 / 19.4,
+// 24.1 / 29.9, 24.7 / 33.9.)
 static int parts_of(const W4Args &a)
 {
-    if (a.E || w4_rows(a) < 64 || w4_tiles64(a) * ((a.N + 63) / 64) >= 256)
+    if (a.E || w4_rows(a) < 64 || w4_tiles64(a) * ((a.N + 63) / 64) > 128)
         return 1;
     const int64_t tiles = w4_tiles64(a) * ((a.N + 127) / 128), steps = (a.K + 255) / 256;
     int parts = 1;

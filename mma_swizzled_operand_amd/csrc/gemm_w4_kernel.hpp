@@ -624,36 +624,48 @@ hipError_t launch_w4_tile(const W4Args &a, hipStream_t stream)
     return hipGetLastError();
 }
 
-// Columns of a workgroup: as many as leave a workgroup for every compute unit
-// (two, for the longest), since more columns share a copy of A and a step's
-// addresses, and make a wave's part of K and with it its run of steps longer.
-// One row by 16384 x 8192, u4, when chosen: 64 columns 15.9 us (now 13.5), 32
-// in two blocks of a wave 18.5, 32 in two waves 16.9, 128 (half the units) 37;
-// by 4096 x 4096: 16 columns 4.3 us, 32 6.2.
+// Columns of a workgroup.  More columns share a copy of A and a step's
+// addresses, and make a wave's part of K and with it its run of steps longer;
+// fewer make more workgroups.  Time goes by rounds of 256 workgroups, one a
+// compute unit, so a width is taken from where half as many columns would need
+// a second round (16 rows), a little later for tiles of four rows, of which two
+// workgroups share a compute unit.  U4 in groups of 128, us by the number of
+// workgroups:
+//   64 columns / 32, K 8192: one row 128: 12.8 / 9.6, 144: 12.9 / 14.6, 192:
+//   13.2 / 14.6, 256: 13.6 / 14.9; 16 rows 128: 15.3 / 11.5, 144: 15.4 / 17.8;
+//   32 experts of K 4096, two rows each, 160: 10.0 / 8.3, 192: 10.2 / 10.2;
+//   32 / 16, K 8192: one row 128: 9.0 / 7.0, 192: 9.2 / 9.2, 256: 9.5 / 11.1;
+//   16 rows 128: 10.9 / 8.3, 160: 10.9 / 14.6.
+// FP4 falls the same way (64 / 32, one row 128: 11.9 / 9.2, 144: 11.9 / 13.9).
+// 128 columns pay while K is short: half as many workgroups start and end (512
+// of them / 1024, one row by K 1024 9.5 / 9.9, 2048 14.7 / 14.5, 3584 28.7 /
+// 25.0, 8192 77 / 59; 32 experts of 2048 x 2048 16.2 / 17.5, x 4096 38.0 /
+// 32.6).
 template <bool BF16, bool E2M1, int SPAN, int ROWS>
 hipError_t launch_w4_cols(const W4Args &a, hipStream_t stream)
 {
     const int64_t tiles = a.E ? (a.E < a.M ? a.E : a.M) : 1;
     auto enough = [&](int cols, int wgs) { return tiles * ((a.N + cols - 1) / cols) >= wgs; };
-    // (16 rows by 16 columns fill a compute unit's LDS, so more than one such
-    // workgroup each would be a second round)
-    return enough(128, 512)                      ? launch_w4_tile<BF16, E2M1, SPAN, ROWS, 2, 4, 3>(a, stream)
-           : enough(64, 256)                     ? launch_w4_tile<BF16, E2M1, SPAN, ROWS, 2, 2, 3>(a, stream)
-           : enough(32, ROWS == 16 ? 129 : 256) ? launch_w4_tile<BF16, E2M1, SPAN, ROWS, 1, 2, 3>(a, stream)
-                                                 : launch_w4_tile<BF16, E2M1, SPAN, ROWS, 1, 1, 3>(a, stream);
+    constexpr int kWgs = ROWS == 16 ? 129 : 192;
+    return a.K <= 2048 && enough(128, 512) ? launch_w4_tile<BF16, E2M1, SPAN, ROWS, 2, 4, 3>(a, stream)
+           : enough(64, kWgs)              ? launch_w4_tile<BF16, E2M1, SPAN, ROWS, 2, 2, 3>(a, stream)
+           : enough(32, kWgs)              ? launch_w4_tile<BF16, E2M1, SPAN, ROWS, 1, 2, 3>(a, stream)
+                                           : launch_w4_tile<BF16, E2M1, SPAN, ROWS, 1, 1, 3>(a, stream);
 }
 
 template <bool BF16, bool E2M1, int SPAN>
 hipError_t launch_w4_span(const W4Args &a, hipStream_t stream)
 {
     const int rows = w4_rows(a);
-    // 64 rows by 128 columns, K split over workgroups where those are too few;
-    // by 64 where these alone fill the chip (64 rows by 16384 x 8192, FP4: 25.6
-    // us, against 22.6 and the sum over two parts of K, 4.9)
+    // 64 rows by 128 columns where K is split (gemm_w4.hip) and where
+    // workgroups of 64 columns would be a second round (64 rows by K 8192, U4,
+    // 257 of those / 129 of 128: 58.4 / 52.6 us, 512: 67.6 / 62.9, 640: 95 /
+    // 107; FP4 45.9 / 37.6, 61.1 / 49.4, 87.1 / 83.9), by 64 up to one round
+    // (600 rows of 32 experts of 512 x 4096, 256 of those / 128: 22.2 / 33.3)
     if (rows == 64)
-        return a.parts > 1                                  ? launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 4, 3, true>(a, stream)
-               : w4_tiles64(a) * ((a.N + 63) / 64) >= 512 ? launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 4, 3>(a, stream)
-                                                            : launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 2, 2>(a, stream);
+        return a.parts > 1                                 ? launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 4, 3, true>(a, stream)
+               : w4_tiles64(a) * ((a.N + 63) / 64) > 256 ? launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 4, 3>(a, stream)
+                                                           : launch_w4_tile<BF16, E2M1, SPAN, 64, 2, 2, 2>(a, stream);
     return rows == 16 ? launch_w4_cols<BF16, E2M1, SPAN, 16>(a, stream) : launch_w4_cols<BF16, E2M1, SPAN, 4>(a, stream);
 }
 

@@ -972,6 +972,8 @@ def test_w4_many_steps(a, w, G, steps):
     (64, 16400, 4640, 32, "bf16", "e2m1", "bf16"), (50, 16400, 4640, 64, "bf16", "u4", "bf16"),
     (64, 16390, 2560, 128, "f16", "u4", "f32"), (64, 32900, 1120, 32, "bf16", "e2m1", "f32"),
     (33, 32800, 1536, 32, "f16", "e2m1", "f32"), (130, 16400, 1312, 128, "bf16", "u4", "f32"),
+    (64, 9000, 4640, 32, "bf16", "e2m1", "bf16"), (50, 12100, 2560, 64, "bf16", "u4", "f32"),
+    (64, 8200, 3584, 128, "f16", "u4", "f32"), (64, 8190, 3584, 32, "f16", "e2m1", "f32"),
     (64, 700, 8224, 32, "bf16", "e2m1", "bf16"), (20, 260, 12320, 64, "bf16", "u4", "f32"),
 ])
 def test_w4_one_matrix_many_steps(M, N, K, G, a, w, d):
