@@ -12,15 +12,15 @@
 // K a group is the K range of its own output matrix.  The buffer ranges end
 // with the group, so rows of the next one read as zeros.
 //
-// 16384 rows of 16 equal groups by 4096 x 2048, bf16: 243 us, 1130 TFLOP/s (a
-// library product of those sizes without groups: 189 to 218); uneven groups,
-// whose last tiles are partly filled, 270.  A step takes 1.9 us, in which the
+// 16384 rows of 16 equal groups by 4096 x 2048, bf16: 241 to 256 us by card,
+// 1140 to 1070 TFLOP/s (a library product of those sizes without groups: 189 to
+// 218); uneven groups, whose last tiles are partly filled, 267 to 287.  A step takes 1.9 us, in which the
 // copies bring 64 KiB into each compute unit and the matrix units are busy for
 // 0.9: it is bound by the copies' way through the L2 and by waiting for the
 // slowest of them at each barrier.  One workgroup per compute unit that goes
 // from tile to tile and starts the next one's copies before it stores the last
-// took 252, since tiles were then dealt out beforehand; K tails checked in
-// every copy, instead of in a step of their own, 257.
+// took 4 % longer, since tiles were then dealt out beforehand; K tails checked in
+// every copy, instead of in a step of their own, 6 %.
 #pragma once
 #include "experts.hpp"
 #include "gemm256_kernel.hpp"

@@ -23,10 +23,12 @@
 // longer than the weights: one row by 16384 x 8192 in 33 us, 18 us without.)
 //
 // Now, inputs changed from call to call: one row by 16384 x 8192, U4 in groups
-// of 128, 13.5 us (70 MB at 5.2 TB/s, memory bound); 64 rows, FP4, 25.2 us (74
-// MB, and 256 MB of A from L2, which is the longer part); 32 experts of 4096 x
-// 2048 and two rows each, U4 in groups of 64, 34.2 us (125 MB at 3.7 TB/s, the
-// scales' short pieces and many short workgroups).
+// of 128, 13.7 us (70 MB at 5.1 TB/s, memory bound); 64 rows, FP4, 24.7 to 29.4
+// us by card (74 MB, and 256 MB of A from L2, which is the longer part), U4
+// 31.4; 32 experts of 4096 x 2048 and two rows each, U4 in groups of 64, 33.0 us
+// (125 MB at 3.8 TB/s, the scales' short pieces and many short workgroups); 512
+// rows by 16384 x 8192, U4 214, FP4 157 (the weights converted once per 64
+// rows, matrix units 38 and 35 % busy).
 //
 // Lane l = (r, q) = (l % 16, l / 16) loads 16 bytes of weight row r, K block q
 // (32 values) of the wave's 128.  MFMA j multiplies dword j of every lane.  The
