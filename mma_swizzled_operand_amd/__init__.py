@@ -20,15 +20,16 @@ import ctypes
 import os
 import threading
 
-from . import _build, experts
+from . import _build, experts, fp8
 from .experts import *  # noqa: F401,F403
+from .fp8 import *  # noqa: F401,F403
 
 __all__ = [
     "DTYPES", "MAJORS", "MswzError", "Plan", "gemm_plan_create", "gemm_plan_create_ld", "gemm_run",
     "gemm_run_blockscaled", "gemm_run_opts", "gemm_run_ws", "gemm_run_ws_noalloc", "gemm_noalloc_scratch_bytes", "GemmOpts", "gemm_plan_destroy", "gemm_status_str", "gemm_plan_describe",
     "gemm_plan_set_scale_major",
     "desc_address", "desc_check", "tile_offset", "lds_lanes", "library_path", "load",
-    *experts.__all__,
+    *experts.__all__, *fp8.__all__,
 ]
 
 DTYPES = {"f16": 1, "bf16": 2, "e4m3": 3, "f32": 4, "e2m1": 5, "e2m3": 6, "e3m2": 7, "e2m1p": 8}
@@ -106,6 +107,7 @@ def load():
         h.mswz_lds_lanes.argtypes = [c_int, c_int, c_int, ctypes.POINTER(ctypes.c_uint32), c_int]
         h.mswz_lds_lanes.restype = c_int
         experts.declare(h)
+        fp8.declare(h)
         _lib = h
         return _lib
 

@@ -67,6 +67,29 @@ hipError_t launch_grouped_m_f16(const GroupedArgs &a, hipStream_t stream);
 hipError_t launch_grouped_k_bf16(const GroupedArgs &a, hipStream_t stream);
 hipError_t launch_grouped_k_f16(const GroupedArgs &a, hipStream_t stream);
 
+// choices (tokens times choices of each) that a layer takes
+constexpr int kLayerChoices = 1024;
+enum LayerAct { kActSilu = 0, kActGelu = 1 };
+
+struct LayerArgs {
+    const void *X;           // [T][ldx]
+    const int32_t *ids;      // [T][topk]
+    const float *w;          // [T][topk]
+    const void *W1;          // [E][2I][H]
+    const float *S1;         // e4m3: [E][2][ceil(I/128)][ceil(H/128)]
+    const void *W2;          // [E][H][I]
+    const float *S2;         // e4m3: [E][ceil(H/128)][ceil(I/128)]
+    void *Y;                 // [T][ldx]
+    void *table, *h;         // parts of the workspace
+    int T, topk, E, H, I;
+    int64_t ldx;
+    int act;                 // LayerAct
+    bool bf16, e4m3;
+};
+
+int64_t layer_workspace_bytes(const LayerArgs &a);
+hipError_t launch_moe_layer(const LayerArgs &a, void *workspace, hipStream_t stream);
+
 // Bounds of group e in 0 .. rows, whatever the array holds: an expert's rows
 // are [lo, hi), empty where the bounds do not ascend.
 __device__ __forceinline__ void group_bounds(const int32_t *offsets, int e, int rows, int &lo, int &hi)

@@ -1,5 +1,5 @@
-// experts_abi.hip — the C ABI declared in include/mswz_experts.h: plan
-// creation, argument checks and dispatch of the expert operators, in abi.hip's
+// experts_abi.hip — the C ABI declared in include/mswz_experts.h and
+// include/mswz_moe_layer.h: plan creation, argument checks and dispatch of the expert operators, in abi.hip's
 // manner: everything the library cannot run is rejected with a status before
 // any GPU work.
 #include <hip/hip_runtime.h>
@@ -8,6 +8,7 @@
 #include <new>
 
 #include "../../include/mswz_experts.h"
+#include "../../include/mswz_moe_layer.h"
 #include "experts.hpp"
 #include "kernels.hpp"
 
@@ -19,6 +20,9 @@ struct gemm_grouped_plan {
 };
 struct moe_plan {
     mswz::MoeArgs a;
+};
+struct moe_layer_plan {
+    mswz::LayerArgs a;
 };
 
 namespace {
@@ -240,6 +244,70 @@ int moe_combine_grad(const moe_plan *p, const void *dY, const void *Ys, const in
         !aligned(dw, 4))
         return MSWZ_ERR_ALIGN;
     return status(mswz::launch_moe_combine_grad(p->a, dY, Ys, pos, w, dYs, dw, static_cast<hipStream_t>(stream)));
+}
+
+int moe_layer_plan_create(moe_layer_plan **out, int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I, int dt,
+                          int w_dt, int act, int64_t ldx)
+{
+    if (!out)
+        return MSWZ_ERR_INVALID;
+    *out = nullptr;
+    if (T <= 0 || topk <= 0 || E <= 0 || !in_range(H) || !in_range(I) || !known_dt(dt) || !known_dt(w_dt) ||
+        (act != MSWZ_ACT_SILU && act != MSWZ_ACT_GELU) || ldx < 0 || (ldx && ldx < H))
+        return MSWZ_ERR_INVALID;
+    const bool e4m3 = w_dt == MSWZ_DT_E4M3;
+    if (T > mswz::kLayerChoices || topk > mswz::kLayerChoices || T * topk > mswz::kLayerChoices || E > kMaxExperts ||
+        !is16(dt) || (w_dt != dt && !e4m3))
+        return MSWZ_ERR_UNSUPPORTED;
+    // rows of X and of the weights are whole 16-byte pieces; buffers are read with 32-bit offsets
+    const int64_t step = e4m3 ? 16 : 8, size = e4m3 ? 1 : 2;
+    if (H % step != 0 || I % step != 0 || ldx % 8 != 0 || ldx > kMaxLd || 2 * I * H * size >= kMaxBytes ||
+        T * topk * I * 4 >= kMaxBytes || T * (ldx ? ldx : H) * 2 >= kMaxBytes)
+        return MSWZ_ERR_UNSUPPORTED;
+    moe_layer_plan *p = new (std::nothrow) moe_layer_plan{};
+    if (!p)
+        return MSWZ_ERR_INVALID;
+    p->a.T = int(T);
+    p->a.topk = int(topk);
+    p->a.E = int(E);
+    p->a.H = int(H);
+    p->a.I = int(I);
+    p->a.ldx = ldx ? ldx : H;
+    p->a.act = act == MSWZ_ACT_SILU ? mswz::kActSilu : mswz::kActGelu;
+    p->a.bf16 = dt == MSWZ_DT_BF16;
+    p->a.e4m3 = e4m3;
+    *out = p;
+    return MSWZ_OK;
+}
+
+void moe_layer_plan_destroy(moe_layer_plan *p) { delete p; }
+
+int64_t moe_layer_plan_workspace_size(const moe_layer_plan *p)
+{
+    return p ? mswz::layer_workspace_bytes(p->a) : int64_t(MSWZ_ERR_INVALID);
+}
+
+int moe_layer(const moe_layer_plan *p, const void *X, const int32_t *ids, const float *w, const void *W1, const float *S1,
+              const void *W2, const float *S2, void *Y, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (!p || !X || !ids || !w || !W1 || !W2 || !Y || !workspace ||
+        workspace_bytes < mswz::layer_workspace_bytes(p->a))
+        return MSWZ_ERR_INVALID;
+    if (p->a.e4m3 ? !S1 || !S2 : S1 || S2)
+        return MSWZ_ERR_INVALID;
+    if (!aligned(X, 16) || !aligned(ids, 4) || !aligned(w, 4) || !aligned(W1, 16) || !aligned(S1, 4) ||
+        !aligned(W2, 16) || !aligned(S2, 4) || !aligned(Y, 16) || !aligned(workspace, 16))
+        return MSWZ_ERR_ALIGN;
+    mswz::LayerArgs a = p->a;
+    a.X = X;
+    a.ids = ids;
+    a.w = w;
+    a.W1 = W1;
+    a.S1 = S1;
+    a.W2 = W2;
+    a.S2 = S2;
+    a.Y = Y;
+    return status(mswz::launch_moe_layer(a, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

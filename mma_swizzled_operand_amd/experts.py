@@ -1,6 +1,6 @@
-"""Binding of the expert operators (include/mswz_experts.h): products with
-4-bit weights, products over rows grouped by expert, and the token movement
-around them.  Names and arguments are the C ABI's.  Tensors are checked against
+"""Binding of the expert operators (include/mswz_experts.h, mswz_moe_layer.h): products with
+4-bit weights, products over rows grouped by expert, the token movement around
+them, and a whole layer of experts for a few tokens.  Names and arguments are the C ABI's.  Tensors are checked against
 the plan's sizes and types and must share one GPU; a call runs on that GPU, on
 ``stream`` (default: torch's current stream of that GPU).
 
@@ -9,6 +9,9 @@ the plan's sizes and types and must share one GPU; a call runs on that GPU, on
     up = gemm_grouped_plan_create(E, T * topk, N, H, "bf16", "bf16")
     gemm_run_grouped(up, Xs, B, offsets, Ys)                  # Ys[p] = Xs[p] . B[e]^T
     moe_combine(moe_plan_create(T, topk, E, N, "bf16"), Ys, pos, Y, weights=w)
+
+    layer = moe_layer_plan_create(T, topk, E, H, I, "bf16")   # decoding
+    moe_layer(layer, X, ids, w, W1, W2, Y, workspace=workspace)
 """
 from __future__ import annotations
 
@@ -17,12 +20,14 @@ import functools
 
 torch = None    # imported by the first call that takes tensors; the package and its plans work without it
 
-__all__ = ["W4Plan", "GroupedPlan", "MoePlan", "gemm_w4_plan_create", "gemm_run_w4", "gemm_grouped_plan_create",
-           "gemm_run_grouped", "moe_plan_create", "moe_dispatch", "moe_combine", "moe_combine_grad"]
+__all__ = ["W4Plan", "GroupedPlan", "MoePlan", "LayerPlan", "gemm_w4_plan_create", "gemm_run_w4", "gemm_grouped_plan_create",
+           "gemm_run_grouped", "moe_plan_create", "moe_dispatch", "moe_combine", "moe_combine_grad",
+           "moe_layer_plan_create", "moe_layer"]
 
 _TORCH = {"f16": "float16", "bf16": "bfloat16", "f32": "float32"}
 _WEIGHTS = {"u4": 9, "e2m1": 5}
 _AXES = {"m": 0, "k": 1}
+_ACTS = {"silu": 0, "gelu": 1}
 
 
 def declare(h):
@@ -42,7 +47,11 @@ def declare(h):
             ("moe_plan_workspace_size", [vp], i64),
             ("moe_dispatch", [vp, vp, vp, vp, vp, vp, vp, vp, i64, vp], c_int),
             ("moe_combine", [vp, vp, vp, vp, vp, vp], c_int),
-            ("moe_combine_grad", [vp, vp, vp, vp, vp, vp, vp, vp], c_int)):
+            ("moe_combine_grad", [vp, vp, vp, vp, vp, vp, vp, vp], c_int),
+            ("moe_layer_plan_create", [out, i64, i64, i64, i64, i64, c_int, c_int, c_int, i64], c_int),
+            ("moe_layer_plan_destroy", [vp], None),
+            ("moe_layer_plan_workspace_size", [vp], i64),
+            ("moe_layer", [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp], c_int)):
         f = getattr(h, name)
         f.argtypes, f.restype = args, res
 
@@ -177,6 +186,28 @@ class MoePlan(_Plan):
         return self.ws_bytes
 
 
+class LayerPlan(_Plan):
+    """A whole gated layer of E experts for T tokens of topk choices each (moe_layer_plan_create)."""
+    _make, _free = "moe_layer_plan_create", "moe_layer_plan_destroy"
+    type = _type("dt")
+
+    def __init__(self, T, topk, E, H, I, dt="bf16", w_dt=None, act="silu", ldx=0):
+        w_dt = w_dt or dt
+        self.T, self.topk, self.E, self.H, self.I = int(T), int(topk), int(E), int(H), int(I)
+        self._create(self.T, self.topk, self.E, self.H, self.I, _dt(dt), _dt(w_dt), _pick(_ACTS, act, "activation"),
+                     int(ldx))
+        self.dt, self.w_dt, self.act, self.ldx = dt, w_dt, act, int(ldx) or self.H
+        self.choices = self.T * self.topk
+        self.w1_numel = self.E * 2 * self.I * self.H
+        tiles = self.E * -(-self.I // 128) * -(-self.H // 128)
+        self.s1_numel, self.s2_numel = 2 * tiles, tiles
+        self.ws_bytes, self._run = int(self._lib.moe_layer_plan_workspace_size(self._h)), self._lib.moe_layer
+
+    def workspace_bytes(self) -> int:
+        """Device workspace moe_layer needs for this plan."""
+        return self.ws_bytes
+
+
 def gemm_w4_plan_create(M, N, K, a_dt="bf16", w_dt="u4", d_dt="bf16", group=128, experts=0, lda=0, ldd=0) -> W4Plan:
     """Plan of D = beta*D + A . dequant(B)^T, B in 4 bits with group scales; experts > 0: one B per expert and
     rows sorted by expert."""
@@ -192,6 +223,12 @@ def gemm_grouped_plan_create(E, M, N, K, dt="bf16", d_dt="f32", axis="m", b_majo
 def moe_plan_create(T, topk, E, H, dt="bf16", ldx=0) -> MoePlan:
     """Plan of moe_dispatch, moe_combine and moe_combine_grad."""
     return MoePlan(T, topk, E, H, dt, ldx)
+
+
+def moe_layer_plan_create(T, topk, E, H, I, dt="bf16", w_dt=None, act="silu", ldx=0) -> LayerPlan:
+    """Plan of moe_layer: W1 [E][2I][H] and W2 [E][H][I] in w_dt (dt, or "e4m3" with a scale per 128 x 128 tile),
+    activation "silu" or "gelu" of the gate."""
+    return LayerPlan(T, topk, E, H, I, dt, w_dt, act, ldx)
 
 
 def _packed(t, dtype, numel, dev, name):
@@ -318,3 +355,23 @@ def moe_combine_grad(plan: MoePlan, dY, Ys, pos, weights, dYs, dw, stream=None) 
           _rows(dY, plan.type, plan.T, plan.H, plan.ldx, dev, "dY"), _packed(Ys, plan.type, n * plan.H, dev, "Ys"),
           _packed(pos, torch.int32, n, dev, "pos"), _packed(weights, torch.float32, n, dev, "weights"),
           _packed(dYs, plan.type, n * plan.H, dev, "dYs"), _packed(dw, torch.float32, n, dev, "dw"))
+
+
+def moe_layer(plan: LayerPlan, X, ids, weights, W1, W2, Y, S1=None, S2=None, workspace=None, stream=None) -> None:
+    """Enqueue Y[t] = sum_j weights[t][j] W2[e] (act(W1[e][:I] X[t]) * (W1[e][I:] X[t])), e = ids[t][j].  S1 fp32
+    [E][2][ceil(I/128)][ceil(H/128)] and S2 [E][ceil(H/128)][ceil(I/128)] for E4M3 weights, else None."""
+    dev = _device(plan, LayerPlan, X, "X")
+    e4m3 = plan.w_dt == "e4m3"
+    if (S1 is None) == e4m3 or (S2 is None) == e4m3:
+        raise ValueError("S1 and S2: given exactly for E4M3 weights")
+    bytes_ok = (torch.float8_e4m3fn, torch.uint8)
+    t1, t2 = ((w.dtype if w.dtype in bytes_ok else bytes_ok[0]) if e4m3 else plan.type for w in (W1, W2))
+    n = plan.choices
+    _call(plan._run, "moe_layer", dev, stream, plan._h, _rows(X, plan.type, plan.T, plan.H, plan.ldx, dev, "X"),
+          _packed(ids, torch.int32, n, dev, "ids"), _packed(weights, torch.float32, n, dev, "weights"),
+          _packed(W1, t1, plan.w1_numel, dev, "W1"),
+          None if S1 is None else _packed(S1, torch.float32, plan.s1_numel, dev, "S1"),
+          _packed(W2, t2, plan.w1_numel // 2, dev, "W2"),
+          None if S2 is None else _packed(S2, torch.float32, plan.s2_numel, dev, "S2"),
+          _rows(Y, plan.type, plan.T, plan.H, plan.ldx, dev, "Y"), _workspace(workspace, plan.ws_bytes, dev),
+          plan.ws_bytes)
