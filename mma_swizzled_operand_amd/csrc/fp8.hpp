@@ -25,6 +25,7 @@ struct Fp8Args {
 
 int64_t fp8_workspace_bytes(const Fp8Args &a);
 hipError_t launch_fp8(const Fp8Args &a, hipStream_t stream);
+hipError_t launch_fp8_skinny(const Fp8Args &a, hipStream_t stream);   // up to 64 rows of A
 
 struct QuantArgs {
     const void *X;           // [M][ldx]

@@ -23,6 +23,7 @@
 
 #include "device_common.hpp"
 #include "fp8.hpp"
+#include "gemm256_kernel.hpp"
 #include "kernels.hpp"
 
 namespace mswz {
@@ -43,11 +44,60 @@ __device__ __forceinline__ u32x4 e4m3_to_bf16(uint32_t lo, uint32_t hi)
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))};
 }
 
+// Four consecutive outputs of row m, columns n .. n+3 (those inside D), rounded
+// into D's kind.  vec: whole pieces are aligned (fp8_whole_stores).
+template <int OUT>
+__device__ __forceinline__ void fp8_store_as(const Fp8Args &a, int m, int n, f32x4 v, bool vec)
+{
+    using T = std::conditional_t<OUT == kOutF32, float, std::conditional_t<OUT == kOutBf16, __bf16, _Float16>>;
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    T *const d = static_cast<T *>(a.D) + int64_t(m) * a.ldd + n;
+    if (vec && n + 4 <= a.N) {
+        t4 *const p = reinterpret_cast<t4 *>(d);
+        if (a.beta) {
+            const t4 old = *p;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                v[r] += float(old[r]);
+        }
+        *p = t4{T(v[0]), T(v[1]), T(v[2]), T(v[3])};
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (n + r < a.N)
+                d[r] = T(a.beta ? v[r] + float(d[r]) : v[r]);
+    }
+}
+
+__device__ __forceinline__ void fp8_store(const Fp8Args &a, int m, int n, f32x4 v, bool vec)
+{
+    if (a.out == kOutF32)
+        fp8_store_as<kOutF32>(a, m, n, v, vec);
+    else if (a.out == kOutBf16)
+        fp8_store_as<kOutBf16>(a, m, n, v, vec);
+    else
+        fp8_store_as<kOutF16>(a, m, n, v, vec);
+}
+
+// Whether four columns of D from a multiple of four on are one aligned piece.
+inline bool fp8_whole_stores(const Fp8Args &a)
+{
+    return a.ldd % 4 == 0 && (reinterpret_cast<uintptr_t>(a.D) & (a.out == kOutF32 ? 15 : 7)) == 0;
+}
+
+// The LDS tile's layout: rows of 128 bytes, 16-byte chunk c of row r at place
+// c ^ fp8_key(r).  As layout.hpp's tile_key for the rows of one fragment, but
+// the same for every 16 rows: all fragments of an operand are read from two
+// addresses (the chunk and that ^ 4) plus constants.
+MSWZ_HD constexpr uint32_t fp8_key(uint32_t row) { return (row ^ ((row >> 3) & 1u)) & 7u; }
+// Copy instruction q fills rows 8q .. 8q+7: the chunk that lane l fetches.
+MSWZ_HD constexpr uint32_t fp8_dma_chunk(int q, int lane) { return uint32_t(lane & 7) ^ fp8_key(dma_row(q, lane)); }
+
 // Direct-to-LDS copy of one operand tile, ROWS rows x 128 bytes a step, by W
 // waves: instruction q (wave q % W's) fills 1 KiB, tile rows 8q .. 8q+7, lane l
-// the chunk that the layout puts at its place (dma_chunk).  Rows beyond the
-// operand and chunks beyond K lie at the end of the buffer's range and read
-// as zeros.
+// the chunk that the layout puts at its place (fp8_dma_chunk).  Rows beyond the
+// operand, and in the last, partial block chunks beyond K, lie at the end of
+// the buffer's range and read as zeros.
 template <int ROWS, int W>
 struct Fp8Copy {
     static constexpr int kInstr = ROWS / 8 / W;
@@ -62,25 +112,21 @@ struct Fp8Copy {
 #pragma unroll
         for (int i = 0; i < kInstr; ++i) {
             const int r = int(dma_row(wave + W * i, lane));
-            voff[i] = r < rows ? uint32_t(r) * uint32_t(ld) + dma_chunk(wave + W * i, lane) * 16 : nbytes;
+            voff[i] = r < rows ? uint32_t(r) * uint32_t(ld) + fp8_dma_chunk(wave + W * i, lane) * 16 : nbytes;
         }
         lds_off = tile_off + 8 * wave * kTileRowBytes;
     }
-    // lim: bytes of a row's 128-byte slice inside K (128 but for a last, partial block)
-    __device__ void issue(uint8_t *stage, int step, int lim, int wave, int lane) const
+    // out: lanes whose chunk does not exist in this step
+    __device__ void issue(uint8_t *stage, int step, bool out) const
     {
 #pragma unroll
-        for (int i = 0; i < kInstr; ++i) {
-            uint32_t off = voff[i] + uint32_t(step) * 128;
-            if (lim < 128 && int(16 * dma_chunk(wave + W * i, lane)) >= lim)
-                off = nbytes;
-            buffer_load_lds16(rsrc, stage + lds_off + i * 8 * W * kTileRowBytes, off, 0);
-        }
+        for (int i = 0; i < kInstr; ++i)
+            buffer_load_lds16(rsrc, stage + lds_off + i * 8 * W * kTileRowBytes, out ? nbytes : voff[i], uint32_t(step) * 128);
     }
 };
 
 // BM x BN outputs a workgroup, WM x WN a wave.  ROWB: B's scales belong to
-// rows (else to 128 x 128 tiles).  EXACT: by way of bf16.  OUT, BETA: D.
+// rows (else to 128 x 128 tiles).  EXACT: by way of bf16.  OUT: D's kind.
 template <int BM, int BN, int WM, int WN, bool ROWB, bool EXACT, int OUT>
 __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN))
 gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_part, bool vec)
@@ -100,39 +146,42 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
     tile_of_block(blockIdx.x, tiles_m, tiles_n, group_m, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
     const int wm = (wave / (BN / WN)) * WM, wn = (wave % (BN / WN)) * WN;
-    const int step0 = int(blockIdx.y) * steps_per_part, step1 = min(step0 + steps_per_part, a.kb);
 
     Fp8Copy<BM, W> ca;
     Fp8Copy<BN, W> cb;
     ca.init(a.A, a.lda, m0, min(BM, a.M - m0), a.K, wave, lane, 0);
     cb.init(a.B, a.ldb, n0, min(BN, a.N - n0), a.K, wave, lane, BM * 128);
-    // this lane's scale: base offset and what a step adds (words beyond the
-    // operand, and waves without a slot, read zeros at the end of the range)
+    // this lane's scale word at step 0, and the bytes from one step's to the
+    // next (words beyond the operand, and waves without a slot, read zeros at
+    // the end of the range)
     const bool for_a = wave < kSlotsA;
     const uint32_t s_rows = for_a ? a.M : ROWB ? a.N : (a.N + 127) / 128;
     const uint32_t s_bytes = s_rows * uint32_t(a.kb) * 4;
     const __amdgpu_buffer_rsrc_t s_rsrc = make_rsrc(for_a ? a.SA : a.SB, s_bytes);
-    uint32_t s_row = for_a ? m0 + 64 * wave + lane
-                     : ROWB ? n0 + 64 * (wave - kSlotsA) + lane : n0 / 128 + lane;
+    const uint32_t s_row = for_a ? m0 + 64 * wave + lane
+                           : ROWB ? n0 + 64 * (wave - kSlotsA) + lane : n0 / 128 + lane;
     const bool s_in = wave < kSlotsA + kSlotsB && s_row < s_rows;
-    const uint32_t s_base = s_in ? ((for_a || ROWB) ? s_row : s_row * uint32_t(a.kb)) * 4 : s_bytes;
-    const uint32_t s_step = s_in ? ((for_a || ROWB) ? s_rows * 4 : 4u) : 0u;
+    const uint32_t s_voff = s_in ? ((for_a || ROWB) ? s_row : s_row * uint32_t(a.kb)) * 4 : s_bytes;
+    const uint32_t s_step = (for_a || ROWB) ? s_rows * 4 : 4u;
 
+    const int step0 = int(blockIdx.y) * steps_per_part, step1 = min(step0 + steps_per_part, a.kb);
+    // a partial last block: the lanes whose chunk lies beyond K (the chunk is
+    // the same in all of a wave's instructions, which are an even number of
+    // eight-row groups apart)
+    static_assert(W % 2 == 0, "fp8_dma_chunk does not depend on the instruction");
+    const bool beyond = int(16 * fp8_dma_chunk(wave, lane)) >= a.K % 128 && a.K % 128 != 0;
     auto issue = [&](uint8_t *stage, uint8_t *scales, int step) {
-        const int lim = a.K - step * 128;
-        ca.issue(stage, step, lim, wave, lane);
-        cb.issue(stage, step, lim, wave, lane);
-        buffer_load_lds4(s_rsrc, scales + 256 * wave, s_base + s_step * uint32_t(step), 0);
+        const bool out = step >= step1 || (step == a.kb - 1 && beyond);
+        ca.issue(stage, step, out);
+        cb.issue(stage, step, out);
+        buffer_load_lds4(s_rsrc, scales + 256 * wave, step < step1 ? s_voff : s_bytes, s_step * uint32_t(step));
     };
 
     const int x16 = lane & 15, g = lane >> 4;
-    uint32_t abase[TI], bbase[TJ];
-#pragma unroll
-    for (int i = 0; i < TI; ++i)
-        abase[i] = tile_offset(uint32_t(wm + 16 * i + x16), uint32_t(kblk16(g)));
-#pragma unroll
-    for (int j = 0; j < TJ; ++j)
-        bbase[j] = BM * 128 + tile_offset(uint32_t(wn + 16 * j + x16), uint32_t(kblk16(g)));
+    const uint32_t at = uint32_t(x16) * kTileRowBytes + ((uint32_t(kblk16(g)) ^ fp8_key(x16)) << 4);
+    const uint32_t a_at = uint32_t(wm) * kTileRowBytes + at, b_at = uint32_t(BM + wn) * kTileRowBytes + at;
+    const uint32_t a_at64 = a_at ^ 64, b_at64 = b_at ^ 64;
+    const uint32_t sa_at = 4 * uint32_t(wm + x16), sb_at = 256 * kSlotsA + 4 * uint32_t(ROWB ? wn + 4 * g : wn / 128);
 
     // register r of a lane: column 16j + 4g + r of B's rows, row 16i + x16 of A's
     f32x4 acc[TJ][TI];
@@ -142,71 +191,79 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
         for (int i = 0; i < TI; ++i)
             acc[j][i] = f32x4{};
 
-    auto frag = [&](const uint8_t *s, uint32_t base) {
-        const u32x4 lo = lds_read16(s, base), hi = lds_read16(s, base ^ 64);
-        return i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
-    };
+    // One block.  MFMA m = TJ i + j; a fragment, with its rows' scales, is read
+    // kAhead MFMAs before its first use, and an MFMA's result is added kLag MFMAs
+    // later, when it has left the matrix unit: the order is pinned, so that few
+    // fragments are live beside the accumulators and the vector unit's work
+    // lies between MFMAs.
     auto compute = [&](const uint8_t *s, const uint8_t *scales) {
-        const float *const sa = reinterpret_cast<const float *>(scales) + wm + x16;
-        const float *const sb = reinterpret_cast<const float *>(scales) + 64 * kSlotsA;
-        f32x4 sbv[ROWB ? TJ : 1];
-        float sb_tile = 0.0f;
-        if constexpr (ROWB) {
-#pragma unroll
-            for (int j = 0; j < TJ; ++j)
-                sbv[j] = *reinterpret_cast<const f32x4 *>(sb + wn + 16 * j + 4 * g);
-        } else {
-            sb_tile = sb[BN > 128 ? wn / 128 : 0];
-        }
-        i32x8 bf[TJ];
-#pragma unroll
-        for (int j = 0; j < TJ; ++j)
-            bf[j] = frag(s, bbase[j]);
-#pragma unroll
-        for (int i = 0; i < TI; ++i) {
-            const i32x8 af = frag(s, abase[i]);
-            const float scale = ROWB ? sa[16 * i] : sa[16 * i] * sb_tile;
-#pragma unroll
-            for (int j = 0; j < TJ; ++j) {
-                f32x4 p;
+        constexpr int kAhead = 2, kLag = 3, n = TI * TJ;
+        using Sched = FragSchedule<TI, TJ, kAhead>;
+        auto frag = [&](uint32_t lo_at, uint32_t hi_at) {
+            const u32x4 lo = lds_read16(s, lo_at), hi = lds_read16(s, hi_at);
+            return __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        };
+        auto word = [&](uint32_t off) { return *reinterpret_cast<const float *>(scales + off); };
+        f32x4 sbv[ROWB ? TJ : 1], p[kLag + 1];
+        float sav[TI];
+        const float sb_tile = ROWB ? 1.0f : word(sb_at);
+        i32x8 af[TI], bf[TJ];
+        static_for<0, n + kLag>([&](auto mc) {
+            constexpr int m = decltype(mc)::value;
+            if constexpr (m < n) {
+                constexpr int i = m / TJ, j = m % TJ, c0 = m == 0 ? 0 : Sched::issued(m - 1), c1 = Sched::issued(m);
+                static_for<c0, c1>([&](auto rc) {
+                    constexpr int it = Sched::item(decltype(rc)::value);
+                    if constexpr (it > 0) {
+                        af[it - 1] = frag(a_at + 2048 * (it - 1), a_at64 + 2048 * (it - 1));
+                        sav[it - 1] = word(sa_at + 64 * (it - 1));
+                    } else {
+                        bf[-it - 1] = frag(b_at + 2048 * (-it - 1), b_at64 + 2048 * (-it - 1));
+                        if constexpr (ROWB)
+                            sbv[-it - 1] = *reinterpret_cast<const f32x4 *>(scales + sb_at + 64 * (-it - 1));
+                    }
+                });
                 if constexpr (EXACT) {
-                    p = f32x4{};
+                    f32x4 v = f32x4{};
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        p = mfma_16x16x32<true>(e4m3_to_bf16(bf[j][2 * q], bf[j][2 * q + 1]),
-                                                e4m3_to_bf16(af[2 * q], af[2 * q + 1]), p);
+                        v = mfma_16x16x32<true>(e4m3_to_bf16(bf[j][2 * q], bf[j][2 * q + 1]),
+                                                e4m3_to_bf16(af[i][2 * q], af[i][2 * q + 1]), v);
+                    p[m % (kLag + 1)] = v;
                 } else {
-                    p = mfma_e4m3(bf[j], af);
+                    p[m % (kLag + 1)] = mfma_e4m3(bf[j], af[i]);
                 }
+            }
+            if constexpr (m >= kLag) {
+                constexpr int l = m - kLag, i = l / TJ, j = l % TJ;
+                const f32x4 v = p[l % (kLag + 1)];
+                if constexpr (!ROWB && j == 0)
+                    sav[i] *= sb_tile;
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    acc[j][i][r] = fmaf(p[r], ROWB ? scale * sbv[j][r] : scale, acc[j][i][r]);
+                    acc[j][i][r] = fmaf(v[r], ROWB ? sav[i] * sbv[ROWB ? j : 0][r] : sav[i], acc[j][i][r]);
             }
-        }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    auto step_end = [] {
+        __builtin_amdgcn_sched_barrier(0);
+        lds_barrier_keep_vm<0>();
+        __builtin_amdgcn_sched_barrier(0);
     };
 
-    if (step0 < step1) {
-        issue(lds0, scl0, step0);
-        lds_barrier_keep_vm<0>();
-        for (int k = step0; k < step1; k += 2) {
-            if (k + 1 < step1)
-                issue(lds1, scl1, k + 1);
-            compute(lds0, scl0);
-            lds_barrier_keep_vm<0>();
-            if (k + 1 < step1) {
-                if (k + 2 < step1)
-                    issue(lds0, scl0, k + 2);
-                compute(lds1, scl1);
-                lds_barrier_keep_vm<0>();
-            }
-        }
+    issue(lds0, scl0, step0);
+    step_end();
+    for (int k = step0; k < step1; k += 2) {
+        issue(lds1, scl1, k + 1);
+        compute(lds0, scl0);
+        step_end();
+        issue(lds0, scl0, k + 2);
+        compute(lds1, scl1);
+        step_end();
     }
 
-    using T = std::conditional_t<OUT == kOutF32, float, std::conditional_t<OUT == kOutBf16, __bf16, _Float16>>;
-    typedef T t4 __attribute__((ext_vector_type(4)));
     const bool split = gridDim.y > 1;
-    const int64_t ld = split ? a.N : a.ldd;
-    T *const D = static_cast<T *>(a.D);
     float *const part = a.ws + int64_t(blockIdx.y) * a.M * a.N;
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
@@ -216,27 +273,13 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
 #pragma unroll
         for (int j = 0; j < TJ; ++j) {
             const int n = n0 + wn + 16 * j + 4 * g;
-            const int64_t at = int64_t(m) * ld + n;
-            f32x4 v = acc[j][i];
             if (split) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     if (n + r < a.N)
-                        part[at + r] = v[r];
-            } else if (vec && n + 4 <= a.N) {
-                t4 *const p = reinterpret_cast<t4 *>(D + at);
-                if (a.beta) {
-                    const t4 old = *p;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        v[r] += float(old[r]);
-                }
-                *p = t4{T(v[0]), T(v[1]), T(v[2]), T(v[3])};
+                        part[int64_t(m) * a.N + n + r] = acc[j][i][r];
             } else {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (n + r < a.N)
-                        D[at + r] = T(a.beta ? v[r] + float(D[at + r]) : v[r]);
+                fp8_store_as<OUT>(a, m, n, acc[j][i], vec);
             }
         }
     }
