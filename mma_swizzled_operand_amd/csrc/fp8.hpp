@@ -23,9 +23,12 @@ struct Fp8Args {
     bool tile;               // B's scales belong to 128 x 128 tiles
 };
 
+// floats from one row of a part's sums to the next
+__host__ __device__ constexpr int64_t fp8_part_pitch(int64_t N) { return (N + 3) & ~int64_t(3); }
+
 int64_t fp8_workspace_bytes(const Fp8Args &a);
 hipError_t launch_fp8(const Fp8Args &a, hipStream_t stream);
-hipError_t launch_fp8_skinny(const Fp8Args &a, hipStream_t stream);   // up to 64 rows of A
+hipError_t launch_fp8_skinny(const Fp8Args &a, hipStream_t stream);   // up to 32 rows of A
 
 struct QuantArgs {
     const void *X;           // [M][ldx]

@@ -11,22 +11,93 @@
 namespace mswz {
 namespace {
 
-template <int BM, int BN, int WM, int WN, bool ROWB, int OUT>
-hipError_t launch_tile(const Fp8Args &a, hipStream_t stream)
+int64_t tiles(const Fp8Args &a, int bm, int bn) { return int64_t((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); }
+
+// Whether a few rows of A take the kernel without barriers
+// (gemm_fp8_skinny.hip): up to 32, unless there are enough tiles of 64 x 64 for
+// the chip, which fetch whole lines (K 4096 by 4096 columns, one row: 7.8 us,
+// tiles 12.4; 16: 8.0 and 12.4; 32: 9.9 and 12.6.  K 8192 by 16384, 16: 32.0 and
+// 31.4; 32: 36.4 and 32.5; 64: 45 and 35).
+bool is_skinny(const Fp8Args &a) { return a.M <= 32 && tiles(a, 64, 64) < (a.M > 16 ? 192 : 256); }
+
+// K parts of a product: where tiles of 64 x 64 leave half of the compute units
+// idle and K is long, it is split until there are as many, each part keeping
+// eight blocks at least (four and twelve: within 3 %).  Unsplit and split: 64 x
+// 2048 x 8192 21.0 and 12.4 us, 64 x 4096 x 4096 12.5 and 10.9, 128 x 4096 x 8192
+// 23.8 and 18.8; with fewer than 24 blocks the second launch takes what the
+// split gives.
+int parts_of(const Fp8Args &a)
 {
-    const int tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN;
-    const dim3 grid(uint32_t(tiles_m) * uint32_t(tiles_n), 1);
-    hipLaunchKernelGGL((gemm_fp8_kernel<BM, BN, WM, WN, ROWB, OUT == kOutF32, OUT>), grid,
-                       dim3(64 * (BM / WM) * (BN / WN)), 0, stream, a, tiles_m, tiles_n, -4, a.kb, fp8_whole_stores(a));
+    const int64_t t = tiles(a, 64, 64);
+    if (is_skinny(a) || t > 128 || a.kb < 24)
+        return 1;
+    const int64_t most = a.kb / 8;
+    return int(256 / t < most ? 256 / t : most);
+}
+
+// D = beta*D + the parts' sums, in part order; four columns a thread.
+__global__ void __launch_bounds__(256)
+fp8_reduce_kernel(Fp8Args a, int parts, bool vec)
+{
+    const int64_t pitch = fp8_part_pitch(a.N), pieces = pitch / 4, all = pieces * a.M;
+    const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (id >= all)
+        return;
+    const int m = int(id / pieces), n = int(id % pieces) * 4;
+    f32x4 v = f32x4{};
+    for (int p = 0; p < parts; ++p)
+        v += *reinterpret_cast<const f32x4 *>(a.ws + (int64_t(p) * a.M + m) * pitch + n);
+    fp8_store(a, m, n, v, vec);
+}
+
+template <int BM, int BN, int WM, int WN, int S, bool ROWB, int OUT>
+hipError_t launch_tile(const Fp8Args &a, hipStream_t stream, int parts = 1)
+{
+    const int tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN, per = (a.kb + parts - 1) / parts;
+    parts = (a.kb + per - 1) / per;
+    hipLaunchKernelGGL((gemm_fp8_kernel<BM, BN, WM, WN, S, ROWB, OUT == kOutF32, OUT>),
+                       dim3(uint32_t(tiles_m) * uint32_t(tiles_n), parts), dim3(64 * (BM / WM) * (BN / WN)), 0, stream, a,
+                       tiles_m, tiles_n, -4, per, fp8_whole_stores(a));
+    if (parts > 1)
+        hipLaunchKernelGGL(fp8_reduce_kernel, dim3(uint32_t((fp8_part_pitch(a.N) / 4 * a.M + 255) / 256)), dim3(256), 0,
+                           stream, a, parts, fp8_whole_stores(a));
     return hipGetLastError();
 }
 
 template <bool ROWB, int OUT>
 hipError_t launch_out(const Fp8Args &a, hipStream_t stream)
 {
-    if (int64_t((a.M + 255) / 256) * ((a.N + 255) / 256) >= 256)
-        return launch_tile<256, 256, 128, 64, ROWB, OUT>(a, stream);
-    return launch_tile<128, 128, 64, 64, ROWB, OUT>(a, stream);
+    const int parts = parts_of(a);
+    if (parts > 1)
+        return launch_tile<64, 64, 32, 32, 4, ROWB, OUT>(a, stream, parts);
+    // The tile whose rounds over the chip take the least time.  A tile's time,
+    // in units of 10 ns for one block of K, is what one round took (K 4096, 16-bit
+    // D); the compute units hold one workgroup each but for the tile of 128 x 128
+    // by four waves, of which they hold two.  (4096 x 4096 x 4096: 137, 125, 97, 88
+    // and 67 us in this order; 256 x 4096 x 4096: 13.7, 18, 23, 31, 56; 1024 x 4096
+    // x 4096: 38, 35, 25, 34, 57; 4096 x 2048 x 4096: 68, 66, 49, 45, 59.)  The
+    // largest does not leave the bf16 form registers, so an fp32 D stops at 128
+    // x 128 (4096 x 4096 x 4096 147 us, 238 with it).
+    const struct {
+        int64_t rounds, time;
+    } all[5] = {{(tiles(a, 64, 64) + 255) / 256, 25},
+                {(tiles(a, 128, 64) + 255) / 256, 42},
+                {(tiles(a, 128, 128) + 255) / 256, 72},
+                {(tiles(a, 128, 128) + 511) / 512, 123},
+                {(tiles(a, 256, 256) + 255) / 256, 200}};
+    int best = 0;
+    for (int i = 1; i < (OUT == kOutF32 ? 4 : 5); ++i)
+        if (all[i].rounds * all[i].time <= all[best].rounds * all[best].time)
+            best = i;
+    switch (best) {
+    case 0: return launch_tile<64, 64, 32, 32, 4, ROWB, OUT>(a, stream);
+    case 1: return launch_tile<128, 64, 32, 32, 4, ROWB, OUT>(a, stream);
+    case 2: return launch_tile<128, 128, 64, 32, 4, ROWB, OUT>(a, stream);
+    case 3: return launch_tile<128, 128, 64, 64, 2, ROWB, OUT>(a, stream);
+    }
+    if constexpr (OUT != kOutF32)
+        return launch_tile<256, 256, 128, 64, 2, ROWB, OUT>(a, stream);
+    return hipErrorUnknown;
 }
 
 template <bool ROWB>
@@ -38,11 +109,15 @@ hipError_t launch_rows(const Fp8Args &a, hipStream_t stream)
 
 }  // namespace
 
-int64_t fp8_workspace_bytes(const Fp8Args &) { return 0; }
+int64_t fp8_workspace_bytes(const Fp8Args &a)
+{
+    const int parts = parts_of(a);
+    return parts > 1 ? parts * a.M * fp8_part_pitch(a.N) * 4 : 0;
+}
 
 hipError_t launch_fp8(const Fp8Args &a, hipStream_t stream)
 {
-    if (a.M <= 64)
+    if (is_skinny(a))
         return launch_fp8_skinny(a, stream);
     return a.tile ? launch_rows<false>(a, stream) : launch_rows<true>(a, stream);
 }

@@ -19,6 +19,7 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include <tuple>
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -125,9 +126,9 @@ struct Fp8Copy {
     }
 };
 
-// BM x BN outputs a workgroup, WM x WN a wave.  ROWB: B's scales belong to
+// BM x BN outputs a workgroup, WM x WN a wave, S stages in LDS.  ROWB: B's scales belong to
 // rows (else to 128 x 128 tiles).  EXACT: by way of bf16.  OUT: D's kind.
-template <int BM, int BN, int WM, int WN, bool ROWB, bool EXACT, int OUT>
+template <int BM, int BN, int WM, int WN, int S, bool ROWB, bool EXACT, int OUT>
 __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN))
 gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_part, bool vec)
 {
@@ -136,12 +137,19 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
     // scale words of a step: wave w copies 64 of them into slot w of the stage
     constexpr int kSlotsA = BM / 64, kSlotsB = ROWB ? BN / 64 : 1;
     static_assert(kSlotsA + kSlotsB <= W, "one instruction a wave");
+    // (arrays of their own: reads of one stage do not wait for copies into another)
     __shared__ __attribute__((aligned(1024))) uint8_t lds0[kAB];
     __shared__ __attribute__((aligned(1024))) uint8_t lds1[kAB];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds2[S > 2 ? kAB : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds3[S > 3 ? kAB : 16];
     __shared__ __attribute__((aligned(256))) uint8_t scl0[256 * W];
     __shared__ __attribute__((aligned(256))) uint8_t scl1[256 * W];
+    __shared__ __attribute__((aligned(256))) uint8_t scl2[S > 2 ? 256 * W : 16];
+    __shared__ __attribute__((aligned(256))) uint8_t scl3[S > 3 ? 256 * W : 16];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    auto stage = [&](auto n) { return std::get<decltype(n)::value>(std::make_tuple(lds0, lds1, lds2, lds3)); };
+    auto scales_of = [&](auto n) { return std::get<decltype(n)::value>(std::make_tuple(scl0, scl1, scl2, scl3)); };
     int tm, tn;
     tile_of_block(blockIdx.x, tiles_m, tiles_n, group_m, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
@@ -246,25 +254,31 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
             __builtin_amdgcn_sched_barrier(0);
         });
     };
+    // a step ends when the next one's copies are in LDS; those of the S - 2
+    // steps after it stay in flight
+    constexpr int kCopies = decltype(ca)::kInstr + decltype(cb)::kInstr + 1;
     auto step_end = [] {
         __builtin_amdgcn_sched_barrier(0);
-        lds_barrier_keep_vm<0>();
+        lds_barrier_keep_vm<(S - 2) * kCopies>();
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    issue(lds0, scl0, step0);
+    static_for<0, S - 1>([&](auto n) { issue(stage(n), scales_of(n), step0 + n); });
     step_end();
-    for (int k = step0; k < step1; k += 2) {
-        issue(lds1, scl1, k + 1);
-        compute(lds0, scl0);
-        step_end();
-        issue(lds0, scl0, k + 2);
-        compute(lds1, scl1);
-        step_end();
-    }
+    // (steps behind the last are of zeros)
+    for (int k = step0; k < step1; k += S)
+        static_for<0, S>([&](auto n) {
+            constexpr int next = (n + S - 1) % S;
+            issue(stage(std::integral_constant<int, next>{}), scales_of(std::integral_constant<int, next>{}), k + n + S - 1);
+            compute(stage(n), scales_of(n));
+            step_end();
+        });
+    lds_barrier_keep_vm<0>();   // no copy may still be writing LDS when the workgroup ends
 
+    // a part of K leaves its sums in the workspace, in rows of whole 16-byte pieces
     const bool split = gridDim.y > 1;
-    float *const part = a.ws + int64_t(blockIdx.y) * a.M * a.N;
+    const int64_t pitch = fp8_part_pitch(a.N);
+    float *const part = a.ws + int64_t(blockIdx.y) * a.M * pitch;
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
         const int m = m0 + wm + 16 * i + x16;
@@ -274,10 +288,8 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
         for (int j = 0; j < TJ; ++j) {
             const int n = n0 + wn + 16 * j + 4 * g;
             if (split) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (n + r < a.N)
-                        part[int64_t(m) * a.N + n + r] = acc[j][i][r];
+                if (n < a.N)
+                    *reinterpret_cast<f32x4 *>(part + m * pitch + n) = acc[j][i];
             } else {
                 fp8_store_as<OUT>(a, m, n, acc[j][i], vec);
             }

@@ -1,5 +1,5 @@
 // gemm_fp8_skinny.hip — the E4M3 product with a scale per block of 128 for up
-// to 64 rows of A (decoding): B is streamed once from memory straight into
+// to 32 rows of A (decoding): B is streamed once from memory straight into
 // registers.
 //
 // One workgroup of eight waves owns all rows of A and 16*R rows of B; its waves
@@ -27,7 +27,7 @@ gemm_fp8_skinny_kernel(Fp8Args a, bool vec)
 {
     constexpr int W = kSkinnyWaves;
     constexpr int kRegs = 8 * (R + NT) + NT + (ROWB ? 4 * R : 1);
-    constexpr int kDepth = 4 * kRegs <= 144 ? 4 : 3 * kRegs <= 144 ? 3 : 2;
+    constexpr int kDepth = 4 * kRegs <= 120 ? 4 : 3 * kRegs <= 120 ? 3 : 2;
     __shared__ __attribute__((aligned(16))) f32x4 sums[W][R * NT][64];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -49,10 +49,14 @@ gemm_fp8_skinny_kernel(Fp8Args a, bool vec)
         u32x4 b[R][2], x[NT][2];
         float sa[NT], sb[ROWB ? 4 * R : 1];
     };
-    // block u of this wave, zeros behind its last (what lies behind an operand
-    // is asked for at the end of the buffer's range, which reads zeros)
-    auto load = [&](Block &d, int u) {
-        const bool none = u >= u1;
+    // the i-th block of this wave, zeros behind its last (what lies behind an
+    // operand is asked for at the end of the buffer's range, which reads zeros)
+    // (workgroups start at different blocks: rows a power of two apart lie in
+    // the same channel of the L2; 2 to 5 %)
+    const int n = u1 - u0, rot = n ? int(blockIdx.x / 8) % n : 0;
+    auto load = [&](Block &d, int i) {
+        const bool none = i >= n;
+        const int u = u0 + i + rot - (i + rot >= n ? n : 0);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const bool out = none || (u == a.kb - 1 && beyond[h]);
@@ -120,8 +124,8 @@ gemm_fp8_skinny_kernel(Fp8Args a, bool vec)
     Block d[kDepth];
 #pragma unroll
     for (int i = 0; i < kDepth; ++i)
-        load(d[i], u0 + i);
-    for (int u = u0; u < u1; u += kDepth) {
+        load(d[i], i);
+    for (int u = 0; u < n; u += kDepth) {
 #pragma unroll
         for (int i = 0; i < kDepth; ++i) {
             compute(d[i]);
@@ -136,13 +140,13 @@ gemm_fp8_skinny_kernel(Fp8Args a, bool vec)
     __syncthreads();
     // four columns a thread, a row's 16 R columns side by side
     for (int id = threadIdx.x; id < R * NT * 64; id += 64 * W) {
-        const int m = id / (4 * R), n4 = id % (4 * R), n = n0 + 4 * n4;
+        const int m = id / (4 * R), n4 = id % (4 * R), col = n0 + 4 * n4;
         f32x4 v = f32x4{};
 #pragma unroll
         for (int w = 0; w < W; ++w)
             v += sums[w][(n4 / 4) * NT + m / 16][(n4 % 4) * 16 + m % 16];
-        if (m < a.M && n < a.N)
-            fp8_store(a, m, n, v, vec);
+        if (m < a.M && col < a.N)
+            fp8_store(a, m, col, v, vec);
     }
 }
 
@@ -168,9 +172,11 @@ hipError_t launch(const Fp8Args &a, hipStream_t stream)
 template <int NT>
 hipError_t launch_cols(const Fp8Args &a, hipStream_t stream)
 {
-    if (a.N >= 256 * 64)
-        return launch<4, NT>(a, stream);
-    if (a.N >= 256 * 32)
+    // 32 columns a workgroup read A half as often: worth it for more than a few
+    // rows where there are enough workgroups (K 4096 by 8192 columns, 16 rows:
+    // 11.8 us, 13.6 with 16 columns; 32 rows: 14.5 and 18.9; one row, K 8192: 19.8
+    // and 16.9)
+    if (a.M > 4 && a.N >= 256 * 32)
         return launch<2, NT>(a, stream);
     return launch<1, NT>(a, stream);
 }
@@ -179,7 +185,7 @@ hipError_t launch_cols(const Fp8Args &a, hipStream_t stream)
 
 hipError_t launch_fp8_skinny(const Fp8Args &a, hipStream_t stream)
 {
-    return a.M > 32 ? launch_cols<4>(a, stream) : a.M > 16 ? launch_cols<2>(a, stream) : launch_cols<1>(a, stream);
+    return a.M > 16 ? launch_cols<2>(a, stream) : launch_cols<1>(a, stream);
 }
 
 }  // namespace mswz
