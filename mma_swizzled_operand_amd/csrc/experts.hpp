@@ -81,6 +81,7 @@ struct LayerArgs {
     const float *S2;         // e4m3: [E][ceil(H/128)][ceil(I/128)]
     void *Y;                 // [T][ldx]
     void *table, *h;         // parts of the workspace
+    float *rows;             // [T * topk][H]
     int T, topk, E, H, I;
     int64_t ldx;
     int act;                 // LayerAct

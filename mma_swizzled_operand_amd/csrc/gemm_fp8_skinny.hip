@@ -123,13 +123,16 @@ gemm_fp8_skinny_kernel(Fp8Args a, bool vec)
 
     Block d[kDepth];
 #pragma unroll
-    for (int i = 0; i < kDepth; ++i)
+    for (int i = 0; i < kDepth; ++i) {
         load(d[i], i);
+        __builtin_amdgcn_sched_barrier(0);   // (the loads stay in the order of their use)
+    }
     for (int u = 0; u < n; u += kDepth) {
 #pragma unroll
         for (int i = 0; i < kDepth; ++i) {
             compute(d[i]);
             load(d[i], u + i + kDepth);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 #pragma unroll

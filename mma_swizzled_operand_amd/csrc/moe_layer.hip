@@ -1,12 +1,16 @@
-// moe_layer.hip — a gated layer of experts for a few tokens, in two kernels:
+// moe_layer.hip — a gated layer of experts for a few tokens, in two kernels
+// (three for more than a few choices):
 //     h[c]  = act(W1[e][:I] x) * (W1[e][I:] x)        for each choice c = (t, j), e = ids[t][j]
 //     y[t]  = sum_j w[t][j] W2[e] h[c]
 //
 // With a few tokens the time is that of reading the chosen experts' weights
-// once.  A workgroup owns 16 columns of h (or of y), its eight waves split
-// the inner size between them, and each lane loads its weight rows' pieces
-// straight into registers, without a barrier until the waves' sums meet.  The
-// rows of an expert are found from the ids by the workgroups themselves.
+// once.  A workgroup of the first kernel owns 16 columns of h for one expert,
+// its eight waves split the inner size between them, and each lane loads its
+// weight rows' pieces straight into registers, several units ahead, without a
+// barrier until the waves' sums meet.  The rows of an expert are found from
+// the ids by the workgroups themselves.  The second kernel owns 16 columns of y
+// for all experts, whose sums meet in LDS; with more than a few choices it owns
+// 32 columns for one expert, and a third one adds up a token's choices.
 //
 // 16x16x32 MFMAs, the weights first: lane l holds 8 values of weight row
 // l % 16 (of token l % 16 as the second operand), and its four results are
@@ -24,13 +28,15 @@
 
 #include "device_common.hpp"
 #include "experts.hpp"
+#include "gemm256_kernel.hpp"
 #include "kernels.hpp"
 
 namespace mswz {
 namespace {
 
-constexpr int kWaves = 8, kThreads = 64 * kWaves, kPerWave = kLayerChoices / kWaves;
-constexpr int kCols = 16;   // columns of h or y a workgroup
+constexpr int kDownWaves = 8, kWaves = 4, kThreads = 64 * kWaves, kPerWave = kLayerChoices / kWaves;
+constexpr int kCols = 16;         // columns of h or y a workgroup
+constexpr int kFewChoices = 16;   // choices whose sums meet in LDS (one tile of tokens)
 
 enum Weights { kW16 = 0, kWE4m3 = 1 };
 
@@ -97,21 +103,167 @@ __device__ __forceinline__ void split_f16x8(u32x4 v, u32x4 &hi, u32x4 &lo)
     }
 }
 
-// K elements of a unit, the piece of the inner size that waves share out:
-// one MFMA's for 16-bit weights, a scale's block for E4M3.
+// Tiles of 16 weight rows a wave, and units that it keeps in flight: E4M3 rows
+// are half as long, so more of them share a token's values.
 template <int WK>
-constexpr int unit_k() { return WK == kWE4m3 ? 128 : 32; }
+constexpr int tiles_of() { return WK == kWE4m3 ? 4 : 2; }
+template <int WK>
+constexpr int depth_of(int NT) { return WK == kW16 && NT == 1 ? 4 : 2; }
 
-// The first kernel: 16 columns of h for the choices of one expert, the
-// blockIdx.y-th of those in use.
+// A wave's share of a product of weight rows (TILES tiles of 16) with rows of
+// tokens (NT tiles of 16).  A unit is 64 bytes of every weight row, 32 values of
+// 16 bits or 64 of E4M3; lane l holds 16 bytes of it, at 16 (l/16), and the
+// values of its token's row that meet them.  kDepth units are in flight.  DOWN:
+// the rows are h's two parts, 8 values of the upper part next to the same of the
+// lower; else X's.
+template <bool BF16, int WK, bool DOWN, int TILES, int NT, int kDepth>
+struct Stream {
+    static constexpr int NX = (WK == kWE4m3 ? 2 : 1) * (DOWN ? 2 : 1);   // 16-byte pieces of a token's row a unit
+    // scales of a block: the gate's tiles (even) and the others of h, or one for
+    // all columns of y, which lie in one tile of 128
+    static constexpr int NS = DOWN ? 1 : 2;
+    static_assert(WK == kW16 || kDepth % 2 == 0, "a scale's block is two units");
+    struct Unit {
+        u32x4 w[TILES], x[NT][NX];
+        float s[NS];
+    };
+    __amdgpu_buffer_rsrc_t w_rsrc, x_rsrc, s_rsrc;
+    uint32_t w_row[TILES], s_row[NS], x_row[NT];   // byte offsets of this lane's rows, the end of the range for none
+    uint32_t w_end, x_end, s_end, row_bytes;
+    f32x4 acc[NT][TILES];
+
+    __device__ void load(Unit &d, int u, bool none, int g, bool last) const
+    {
+        const uint32_t at = 64u * uint32_t(u) + 16u * uint32_t(g);
+        const bool out = none || at >= row_bytes;
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+            d.w[t] = buffer_load16(w_rsrc, out ? w_end : w_row[t] + at, 0);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < NX; ++i)
+                d.x[t][i] = buffer_load16(x_rsrc, out || x_row[t] == x_end ? x_end : x_row[t] + NX * at + 16 * i, 0);
+        if constexpr (WK == kWE4m3)
+            if (last)
+#pragma unroll
+                for (int t = 0; t < NS; ++t)
+                    d.s[t] = __builtin_bit_cast(float, buffer_load4(s_rsrc, none ? s_end : s_row[t] + 4u * uint32_t(u / 2), 0));
+    }
+
+    // one MFMA step: 8 values a lane of the weights with those of a token
+    static __device__ __forceinline__ f32x4 step(u32x4 w, const u32x4 *x, f32x4 c)
+    {
+        if constexpr (!DOWN)
+            return mfma_16x16x32<BF16>(w, x[0], c);
+        else if constexpr (BF16 || WK == kWE4m3)
+            return mfma_16x16x32<true>(w, x[1], mfma_16x16x32<true>(w, x[0], c));
+        u32x4 hi, lo;
+        split_f16x8(w, hi, lo);
+        c = mfma_16x16x32<true>(hi, x[1], mfma_16x16x32<true>(hi, x[0], c));
+        return mfma_16x16x32<true>(lo, x[1], mfma_16x16x32<true>(lo, x[0], c));
+    }
+
+    // units u0 .. u1 - 1 (E4M3: both even), the turn-th and the ones after it
+    // first: waves that start at different places do not ask the same channels
+    // of the L2 for the tokens' rows at the same time
+    __device__ void run(int u0, int u1, int turn, int g)
+    {
+        constexpr int per = WK == kWE4m3 ? 2 : 1;
+        const int n = u1 - u0, rot = n > 0 ? turn % (n / per) * per : 0;
+        auto unit = [&](int i) { return u0 + i + rot - (i + rot >= n ? n : 0); };
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < TILES; ++i)
+                acc[t][i] = f32x4{};
+        Unit d[kDepth];
+        static_for<0, kDepth>([&](auto i) {
+            load(d[i], unit(i), i >= n, g, i % 2 == 1);
+            __builtin_amdgcn_sched_barrier(0);   // (the loads stay in the order of their use)
+        });
+        f32x4 part[NT][TILES];
+        for (int u = 0; u < n; u += kDepth)
+            static_for<0, kDepth>([&](auto ic) {
+                constexpr int i = decltype(ic)::value;
+#pragma unroll
+                for (int w = 0; w < TILES; ++w) {
+                    if constexpr (WK == kW16) {
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            acc[t][w] = step(d[i].w[w], d[i].x[t], acc[t][w]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const u32x4 v = from_e4m3<BF16 || DOWN>(d[i].w[w][2 * q], d[i].w[w][2 * q + 1]);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+                                part[t][w] = step(v, d[i].x[t] + q * (NX / 2), i % 2 == 0 && q == 0 ? f32x4{} : part[t][w]);
+                        }
+                        if (i % 2 == 1)
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                for (int r = 0; r < 4; ++r)
+                                    acc[t][w][r] = fmaf(d[i].s[w % NS], part[t][w][r], acc[t][w][r]);
+                    }
+                }
+                load(d[i], unit(u + i + kDepth), u + i + kDepth >= n, g, i % 2 == 1);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+    }
+};
+
+// Calls fn with one or two tiles of 16 rows at a time, rows r0 .. of n.
+template <class Fn>
+__device__ __forceinline__ void by_rows(int n, Fn &&fn)
+{
+    for (int r0 = 0; r0 < n; r0 += 32)
+        if (n - r0 <= 16)
+            fn(r0, std::integral_constant<int, 1>{});
+        else
+            fn(r0, std::integral_constant<int, 2>{});
+}
+
+// The sums of the `parts` waves that share a product, one tile of tokens: the
+// first of them gets them, in their order.
+template <int TILES>
+__device__ __forceinline__ void add_parts(f32x4 (*sums)[TILES][64], f32x4 *v, int wave, int parts, int lane)
+{
+    if (parts == 1)
+        return;
+#pragma unroll
+    for (int i = 0; i < TILES; ++i)
+        sums[wave][i][lane] = v[i];
+    __syncthreads();
+    if (wave % parts == 0)
+        for (int w = 1; w < parts; ++w)
+#pragma unroll
+            for (int i = 0; i < TILES; ++i)
+                v[i] += sums[wave + w][i][lane];
+    __syncthreads();
+}
+
+// The part of a wave among `parts`: units of 64 bytes, whole blocks of a scale.
+template <int WK>
+__device__ __forceinline__ void share(uint32_t row_bytes, int part, int parts, int &u0, int &u1)
+{
+    constexpr int per = WK == kWE4m3 ? 2 : 1;
+    const int units = int((row_bytes + 64 * per - 1) / (64 * per));
+    u0 = per * (units * part / parts);
+    u1 = per * (units * (part + 1) / parts);
+}
+
+// The first kernel: the choices of one expert, the blockIdx.y-th of those in
+// use; 8 * TILES columns of h for every `parts` waves.
 template <bool BF16, int WK>
 __global__ void __launch_bounds__(kThreads)
-moe_layer_up_kernel(LayerArgs a)
+moe_layer_up_kernel(LayerArgs a, int parts)
 {
     __shared__ uint32_t used[32];
     __shared__ int before[2][kWaves];
     __shared__ uint16_t rows[kLayerChoices];
-    __shared__ __attribute__((aligned(16))) f32x4 sums[kWaves][4][2][64];
+    __shared__ __attribute__((aligned(16))) f32x4 sums[kWaves][tiles_of<WK>()][64];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int choices = a.T * a.topk;
@@ -184,221 +336,118 @@ moe_layer_up_kernel(LayerArgs a)
     }
 
     // ---- the products ----
-    constexpr int UK = unit_k<WK>(), kSize = WK == kWE4m3 ? 1 : 2;
-    const int i0 = blockIdx.x * kCols, x16 = lane & 15, g = lane >> 4;
-    const uint32_t row_bytes = uint32_t(a.H) * kSize, w_bytes = 2u * uint32_t(a.I) * row_bytes;
-    const __amdgpu_buffer_rsrc_t w_rsrc = make_rsrc(static_cast<const uint8_t *>(a.W1) + uint64_t(expert) * w_bytes, w_bytes);
-    const uint32_t x_pitch = uint32_t(a.ldx) * 2, x_bytes = uint32_t(a.T - 1) * x_pitch + uint32_t(a.H) * 2;
-    const __amdgpu_buffer_rsrc_t x_rsrc = make_rsrc(a.X, x_bytes);
-    const uint32_t gate = uint32_t(min(i0 + x16, a.I - 1)) * row_bytes, up = gate + uint32_t(a.I) * row_bytes;
-    const int units = (a.H + UK - 1) / UK, u0 = units * wave / kWaves, u1 = units * (wave + 1) / kWaves;
+    constexpr int kSize = WK == kWE4m3 ? 1 : 2;
+    constexpr int TILES = tiles_of<WK>();
+    const int i0 = (int(blockIdx.x) * (kWaves / parts) + wave / parts) * (8 * TILES), x16 = lane & 15, g = lane >> 4;
+    const uint32_t row_bytes = uint32_t(a.H) * kSize, x_pitch = uint32_t(a.ldx) * 2;
     const int ib = (a.I + 127) / 128, hb = (a.H + 127) / 128;
-    const float *const s_gate = WK == kWE4m3 ? a.S1 + (int64_t(expert) * 2 * ib + i0 / 128) * hb : nullptr;
-    const float *const s_up = WK == kWE4m3 ? s_gate + int64_t(ib) * hb : nullptr;
-
-    auto some = [&](int r0, auto tiles) {
+    int u0, u1;
+    share<WK>(row_bytes, wave % parts, parts, u0, u1);
+    if (i0 >= a.I)
+        u1 = u0;   // (this wave's columns lie behind the last)
+    by_rows(n, [&](int r0, auto tiles) {
         constexpr int NT = decltype(tiles)::value;
-        uint32_t xrow[NT];
+        Stream<BF16, WK, false, TILES, NT, depth_of<WK>(NT)> s;
+        s.row_bytes = row_bytes;
+        s.w_end = 2u * uint32_t(a.I) * row_bytes;
+        s.w_rsrc = make_rsrc(static_cast<const uint8_t *>(a.W1) + uint64_t(expert) * s.w_end, s.w_end);
+#pragma unroll
+        for (int c = 0; c < TILES / 2; ++c) {
+            s.w_row[2 * c] = uint32_t(min(i0 + 16 * c + x16, a.I - 1)) * row_bytes;
+            s.w_row[2 * c + 1] = s.w_row[2 * c] + uint32_t(a.I) * row_bytes;
+        }
+        s.x_end = uint32_t(a.T - 1) * x_pitch + uint32_t(a.H) * 2;
+        s.x_rsrc = make_rsrc(a.X, s.x_end);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int r = r0 + 16 * t + x16;
-            xrow[t] = r < n ? uint32_t(rows[r] / a.topk) * x_pitch : x_bytes;
+            s.x_row[t] = r < n ? uint32_t(rows[r] / uint32_t(a.topk)) * x_pitch : s.x_end;
         }
-        f32x4 acc[NT][2];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-            acc[t][0] = acc[t][1] = f32x4{};
-        // (a piece beyond the inner size reads zeros, and so does a token beyond the last)
-        auto x_at = [&](int t, int k) { return buffer_load16(x_rsrc, k < a.H ? xrow[t] + 2 * uint32_t(k) : x_bytes, 0); };
-        if constexpr (WK == kW16) {
-#pragma unroll 4
-            for (int u = u0; u < u1; ++u) {
-                const int k = UK * u + 8 * g;
-                const u32x4 wg = buffer_load16(w_rsrc, k < a.H ? gate + 2 * uint32_t(k) : w_bytes, 0);
-                const u32x4 wu = buffer_load16(w_rsrc, k < a.H ? up + 2 * uint32_t(k) : w_bytes, 0);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const u32x4 x = x_at(t, k);
-                    acc[t][0] = mfma_16x16x32<BF16>(wg, x, acc[t][0]);
-                    acc[t][1] = mfma_16x16x32<BF16>(wu, x, acc[t][1]);
-                }
-            }
-        } else {
-            for (int u = u0; u < u1; ++u) {
-                const float sg = s_gate[u], su = s_up[u];
-                f32x4 part[NT][2];
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    part[t][0] = part[t][1] = f32x4{};
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int k = UK * u + 64 * half + 16 * g;
-                    const u32x4 wg = buffer_load16(w_rsrc, k < a.H ? gate + uint32_t(k) : w_bytes, 0);
-                    const u32x4 wu = buffer_load16(w_rsrc, k < a.H ? up + uint32_t(k) : w_bytes, 0);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            const u32x4 x = x_at(t, k + 8 * q);
-                            part[t][0] = mfma_16x16x32<BF16>(from_e4m3<BF16>(wg[2 * q], wg[2 * q + 1]), x, part[t][0]);
-                            part[t][1] = mfma_16x16x32<BF16>(from_e4m3<BF16>(wu[2 * q], wu[2 * q + 1]), x, part[t][1]);
-                        }
-                }
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        acc[t][0][r] = fmaf(sg, part[t][0][r], acc[t][0][r]);
-                        acc[t][1][r] = fmaf(su, part[t][1][r], acc[t][1][r]);
-                    }
-            }
+        if constexpr (WK == kWE4m3) {
+            s.s_end = 2u * uint32_t(ib) * uint32_t(hb) * 4;
+            s.s_rsrc = make_rsrc(a.S1 + int64_t(expert) * 2 * ib * hb, s.s_end);
+            s.s_row[0] = uint32_t(min(i0, a.I - 1) / 128) * uint32_t(hb) * 4;
+            s.s_row[1] = s.s_row[0] + uint32_t(ib) * uint32_t(hb) * 4;
         }
+        s.run(u0, u1, i0 / (8 * TILES), g);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            sums[wave][t][0][lane] = acc[t][0];
-            sums[wave][t][1][lane] = acc[t][1];
-        }
-        __syncthreads();
-        if (wave < NT) {
-            f32x4 vg = f32x4{}, vu = f32x4{};
-            for (int w = 0; w < kWaves; ++w) {
-                vg += sums[w][wave][0][lane];
-                vu += sums[w][wave][1][lane];
-            }
-            const int r = r0 + 16 * wave + x16, i = i0 + 4 * g;
-            if (r < n && i < a.I) {
+            f32x4 *const v = s.acc[t];
+            add_parts<TILES>(sums, v, wave, parts, lane);
+            const int r = r0 + 16 * t + x16;
+#pragma unroll
+            for (int c = 0; c < TILES / 2; ++c) {
+                const int i = i0 + 16 * c + 4 * g;
+                if (wave % parts != 0 || r >= n || i >= a.I)
+                    continue;
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    split_bf16(activation(vg[e], a.act) * vu[e], hi[e], lo[e]);
+                    split_bf16(activation(v[2 * c][e], a.act) * v[2 * c + 1][e], hi[e], lo[e]);
                 // of every 8 columns the upper parts, then the lower ones
                 uint8_t *const to = static_cast<uint8_t *>(a.h) + (int64_t(rows[r]) * a.I + (i & ~7)) * 4 + 2 * (i & 7);
                 *reinterpret_cast<u32x2 *>(to) = u32x2{hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16)};
                 *reinterpret_cast<u32x2 *>(to + 16) = u32x2{lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16)};
             }
         }
-        __syncthreads();
-    };
-    for (int r0 = 0; r0 < n; r0 += 64) {
-        if (n - r0 <= 16)
-            some(r0, std::integral_constant<int, 1>{});
-        else if (n - r0 <= 32)
-            some(r0, std::integral_constant<int, 2>{});
-        else
-            some(r0, std::integral_constant<int, 4>{});
-    }
+    });
 }
 
-// The second kernel: 16 columns of y for all tokens.  Its waves share out the
-// experts in use and, `splits` ways, the inner size; each choice's sums go to
-// LDS and a token's are added up in the order of its choices.
+// What the second kernels share: TILES tiles of 16 columns of y from h0 on, for
+// the rows r0 .. of an expert's n.
+template <bool BF16, int WK, int TILES, int NT, int kDepth>
+__device__ __forceinline__ Stream<BF16, WK, true, TILES, NT, kDepth>
+down_stream(const LayerArgs &a, int expert, int h0, const int *choice, int x16)
+{
+    const uint32_t row_bytes = uint32_t(a.I) * (WK == kWE4m3 ? 1 : 2);
+    const int ib = (a.I + 127) / 128, hb = (a.H + 127) / 128;
+    Stream<BF16, WK, true, TILES, NT, kDepth> s;
+    s.row_bytes = row_bytes;
+    s.w_end = uint32_t(a.H) * row_bytes;
+    s.w_rsrc = make_rsrc(static_cast<const uint8_t *>(a.W2) + uint64_t(expert) * s.w_end, s.w_end);
+    s.x_end = uint32_t(a.T * a.topk) * uint32_t(a.I) * 4;
+    s.x_rsrc = make_rsrc(a.h, s.x_end);
+    if constexpr (WK == kWE4m3) {
+        s.s_end = uint32_t(hb) * uint32_t(ib) * 4;
+        s.s_rsrc = make_rsrc(a.S2 + int64_t(expert) * hb * ib, s.s_end);
+        s.s_row[0] = uint32_t(min(h0, a.H - 1) / 128) * uint32_t(ib) * 4;
+    }
+#pragma unroll
+    for (int i = 0; i < TILES; ++i)
+        s.w_row[i] = uint32_t(min(h0 + 16 * i + x16, a.H - 1)) * row_bytes;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+        s.x_row[t] = choice[t] >= 0 ? uint32_t(choice[t]) * uint32_t(a.I) * 4 : s.x_end;
+    return s;
+}
+
+// The second kernel for a few choices: 16 columns of y for all tokens.  Its
+// waves share out the experts in use and, `splits` ways, the inner size; each
+// choice's sums go to LDS and a token's are added up in the order of its
+// choices.
 template <bool BF16, int WK>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(64 * kDownWaves)
 moe_layer_down_kernel(LayerArgs a, int splits)
 {
-    extern __shared__ __attribute__((aligned(16))) float of_choice[];   // [splits][choices][16]
+    __shared__ __attribute__((aligned(16))) float of_choice[kDownWaves * kFewChoices * kCols];   // [splits][choices][16]
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int choices = a.T * a.topk;
     const LayerTable *const table = static_cast<const LayerTable *>(a.table);
     const int active = table->active;
-
-    constexpr int UK = unit_k<WK>(), kSize = WK == kWE4m3 ? 1 : 2;
-    const int h0 = blockIdx.x * kCols, x16 = lane & 15, g = lane >> 4;
-    const uint32_t row_bytes = uint32_t(a.I) * kSize, w_bytes = uint32_t(a.H) * row_bytes;
-    const uint32_t wrow = uint32_t(min(h0 + x16, a.H - 1)) * row_bytes;
-    const uint32_t h_bytes = uint32_t(choices) * uint32_t(a.I) * 4;
-    const __amdgpu_buffer_rsrc_t h_rsrc = make_rsrc(a.h, h_bytes);
-    const int split = wave % splits;
-    const int units = (a.I + UK - 1) / UK, u0 = units * split / splits, u1 = units * (split + 1) / splits;
-    const int ib = (a.I + 127) / 128, hb = (a.H + 127) / 128;
-
-    for (int slot = wave / splits; slot < active; slot += kWaves / splits) {
-        const int expert = table->expert[slot], start = table->start[slot], n = table->count[slot];
-        const __amdgpu_buffer_rsrc_t w_rsrc =
-            make_rsrc(static_cast<const uint8_t *>(a.W2) + uint64_t(expert) * w_bytes, w_bytes);
-        const float *const s_row = WK == kWE4m3 ? a.S2 + (int64_t(expert) * hb + h0 / 128) * ib : nullptr;
-        auto some = [&](int r0, auto tiles) {
-            constexpr int NT = decltype(tiles)::value;
-            int choice[NT];
-            uint32_t hrow[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int r = r0 + 16 * t + x16;
-                choice[t] = r < n ? table->order[start + r] : -1;
-                hrow[t] = r < n ? uint32_t(choice[t]) * uint32_t(a.I) * 4 : h_bytes;
-            }
-            f32x4 acc[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                acc[t] = f32x4{};
-            // the parts of h at columns k .. k + 7
-            auto h_at = [&](int t, int k, int part) {
-                return buffer_load16(h_rsrc, k < a.I ? hrow[t] + 4 * uint32_t(k) + 16 * part : h_bytes, 0);
-            };
-            if constexpr (WK == kW16) {
-#pragma unroll 4
-                for (int u = u0; u < u1; ++u) {
-                    const int k = UK * u + 8 * g;
-                    const u32x4 w = buffer_load16(w_rsrc, k < a.I ? wrow + 2 * uint32_t(k) : w_bytes, 0);
-                    u32x4 whi = w, wlo;
-                    if constexpr (!BF16)
-                        split_f16x8(w, whi, wlo);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const u32x4 hi = h_at(t, k, 0), lo = h_at(t, k, 1);
-                        acc[t] = mfma_16x16x32<true>(whi, hi, acc[t]);
-                        acc[t] = mfma_16x16x32<true>(whi, lo, acc[t]);
-                        if constexpr (!BF16) {
-                            acc[t] = mfma_16x16x32<true>(wlo, hi, acc[t]);
-                            acc[t] = mfma_16x16x32<true>(wlo, lo, acc[t]);
-                        }
-                    }
-                }
-            } else {
-                for (int u = u0; u < u1; ++u) {
-                    const float s = s_row[u];
-                    f32x4 part[NT];
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        part[t] = f32x4{};
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int k = UK * u + 64 * half + 16 * g;
-                        const u32x4 w = buffer_load16(w_rsrc, k < a.I ? wrow + uint32_t(k) : w_bytes, 0);
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const u32x4 wq = from_e4m3<true>(w[2 * q], w[2 * q + 1]);
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) {
-                                part[t] = mfma_16x16x32<true>(wq, h_at(t, k + 8 * q, 0), part[t]);
-                                part[t] = mfma_16x16x32<true>(wq, h_at(t, k + 8 * q, 1), part[t]);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            acc[t][r] = fmaf(s, part[t][r], acc[t][r]);
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                if (choice[t] >= 0)
-                    *reinterpret_cast<f32x4 *>(of_choice + (split * choices + choice[t]) * kCols + 4 * g) = acc[t];
-        };
-        for (int r0 = 0; r0 < n; r0 += 64) {
-            if (n - r0 <= 16)
-                some(r0, std::integral_constant<int, 1>{});
-            else if (n - r0 <= 32)
-                some(r0, std::integral_constant<int, 2>{});
-            else
-                some(r0, std::integral_constant<int, 4>{});
-        }
+    const int h0 = blockIdx.x * kCols, x16 = lane & 15, g = lane >> 4, split = wave % splits;
+    int u0, u1;
+    share<WK>(uint32_t(a.I) * (WK == kWE4m3 ? 1 : 2), split, splits, u0, u1);
+    for (int slot = wave / splits; slot < active; slot += kDownWaves / splits) {
+        const int n = table->count[slot];   // (at most kFewChoices, 16)
+        const int choice = x16 < n ? table->order[table->start[slot] + x16] : -1;
+        auto s = down_stream<BF16, WK, 1, 1, 4>(a, table->expert[slot], h0, &choice, x16);
+        s.run(u0, u1, blockIdx.x, g);
+        if (choice >= 0)
+            *reinterpret_cast<f32x4 *>(of_choice + (split * choices + choice) * kCols + 4 * g) = s.acc[0][0];
     }
     __syncthreads();
     using T = std::conditional_t<BF16, __bf16, _Float16>;
-    for (int o = tid; o < a.T * kCols; o += kThreads) {
+    for (int o = tid; o < a.T * kCols; o += 64 * kDownWaves) {
         const int t = o / kCols, col = o % kCols;
         float y = 0.0f;
         for (int j = 0; j < a.topk; ++j) {
@@ -415,25 +464,112 @@ moe_layer_down_kernel(LayerArgs a, int splits)
     }
 }
 
+// The second kernel for more choices: those of one expert, in fp32 rows of the
+// workspace; 16 * TILES columns of y for every `parts` waves.
+template <bool BF16, int WK>
+__global__ void __launch_bounds__(kThreads)
+moe_layer_rows_kernel(LayerArgs a, int parts)
+{
+    constexpr int TILES = tiles_of<WK>();
+    __shared__ __attribute__((aligned(16))) f32x4 sums[kWaves][TILES][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const LayerTable *const table = static_cast<const LayerTable *>(a.table);
+    if (int(blockIdx.y) >= table->active)
+        return;
+    const int expert = table->expert[blockIdx.y], start = table->start[blockIdx.y], n = table->count[blockIdx.y];
+    const int h0 = (int(blockIdx.x) * (kWaves / parts) + wave / parts) * TILES * kCols, x16 = lane & 15, g = lane >> 4;
+    int u0, u1;
+    share<WK>(uint32_t(a.I) * (WK == kWE4m3 ? 1 : 2), wave % parts, parts, u0, u1);
+    if (h0 >= a.H)
+        u1 = u0;   // (this wave's columns lie behind the last)
+    by_rows(n, [&](int r0, auto tiles) {
+        constexpr int NT = decltype(tiles)::value;
+        int choice[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            choice[t] = r0 + 16 * t + x16 < n ? table->order[start + r0 + 16 * t + x16] : -1;
+        auto s = down_stream<BF16, WK, TILES, NT, depth_of<WK>(NT)>(a, expert, h0, choice, x16);
+        s.run(u0, u1, h0 / (TILES * kCols), g);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            f32x4 *const v = s.acc[t];
+            add_parts<TILES>(sums, v, wave, parts, lane);
+            if (wave % parts == 0 && choice[t] >= 0)
+#pragma unroll
+                for (int i = 0; i < TILES; ++i)
+                    if (h0 + 16 * i + 4 * g < a.H)
+                        *reinterpret_cast<f32x4 *>(a.rows + int64_t(choice[t]) * a.H + h0 + 16 * i + 4 * g) = v[i];
+        }
+    });
+}
+
+// y[t] = sum_j w[t][j] rows[t][j], in the order of j; four columns a thread.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+moe_layer_sum_kernel(LayerArgs a)
+{
+    const int t = blockIdx.y, h = (blockIdx.x * 256 + threadIdx.x) * 4;
+    if (h >= a.H)
+        return;
+    f32x4 y = f32x4{};
+    for (int j = 0; j < a.topk; ++j) {
+        const int c = t * a.topk + j;
+        if (uint32_t(a.ids[c]) >= uint32_t(a.E))
+            continue;
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(a.rows + int64_t(c) * a.H + h);
+        const float w = a.w[c];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            y[e] = fmaf(w, v[e], y[e]);
+    }
+    using T = std::conditional_t<BF16, __bf16, _Float16>;
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<t4 *>(static_cast<T *>(a.Y) + int64_t(t) * a.ldx + h) = t4{T(y[0]), T(y[1]), T(y[2]), T(y[3])};
+}
+
 template <bool BF16, int WK>
 hipError_t launch(const LayerArgs &a, hipStream_t stream)
 {
     const int choices = a.T * a.topk, experts = a.E < choices ? a.E : choices;
-    hipLaunchKernelGGL((moe_layer_up_kernel<BF16, WK>), dim3((a.I + kCols - 1) / kCols, experts), dim3(kThreads), 0, stream, a);
-    // waves that share an expert, until the experts in use can be as many as waves
-    int splits = 1;
-    while (splits < kWaves && experts * splits < 2 * kWaves && 2 * splits * choices <= kLayerChoices)
-        splits *= 2;
-    const size_t lds = size_t(splits) * choices * kCols * 4;
-    hipLaunchKernelGGL((moe_layer_down_kernel<BF16, WK>), dim3((a.H + kCols - 1) / kCols), dim3(kThreads), lds, stream, a, splits);
+    const dim3 block(kThreads);
+    // waves that share a product, until there are enough of them for the chip
+    // (28 experts in use of 4096 x 2048 bf16, 16 tokens: 175 and 85 us for the two
+    // kernels with 4096 waves, 155 and 85 with 8192, 146 and 86 with 16384; 64
+    // experts of 2048 x 1024 E4M3, 64 tokens: 72 and 52, 71 and 47, 74 and 45)
+    constexpr int64_t kEnough = WK == kWE4m3 ? 8192 : 16384;
+    auto parts_for = [&](int64_t slabs) {
+        int parts = 1;
+        while (parts < kWaves && experts * slabs * parts < kEnough)
+            parts *= 2;
+        return parts;
+    };
+    auto groups = [](int slabs, int parts) { return uint32_t((slabs + kWaves / parts - 1) / (kWaves / parts)); };
+    constexpr int TILES = tiles_of<WK>();
+    const int slabs = (a.I + 8 * TILES - 1) / (8 * TILES), parts = parts_for(slabs);
+    hipLaunchKernelGGL((moe_layer_up_kernel<BF16, WK>), dim3(groups(slabs, parts), experts), block, 0, stream, a, parts);
+    if (choices <= kFewChoices) {
+        // waves that share an expert, until the experts in use can be as many as waves
+        int splits = 1;
+        while (splits < kDownWaves && experts * splits < kDownWaves)
+            splits *= 2;
+        hipLaunchKernelGGL((moe_layer_down_kernel<BF16, WK>), dim3((a.H + kCols - 1) / kCols), dim3(64 * kDownWaves), 0, stream, a, splits);
+    } else {
+        const int wide = (a.H + TILES * kCols - 1) / (TILES * kCols), shared = parts_for(wide);
+        hipLaunchKernelGGL((moe_layer_rows_kernel<BF16, WK>), dim3(groups(wide, shared), experts), block, 0, stream, a, shared);
+        hipLaunchKernelGGL(moe_layer_sum_kernel<BF16>, dim3((a.H + 1023) / 1024, a.T), dim3(256), 0, stream, a);
+    }
     return hipGetLastError();
 }
+
+// bytes of h, whole 16-byte pieces
+int64_t h_bytes(const LayerArgs &a) { return int64_t(a.T) * a.topk * a.I * 4; }
 
 }  // namespace
 
 int64_t layer_workspace_bytes(const LayerArgs &a)
 {
-    return int64_t(sizeof(LayerTable)) + int64_t(a.T) * a.topk * a.I * 4;
+    const int64_t choices = int64_t(a.T) * a.topk;
+    return int64_t(sizeof(LayerTable)) + h_bytes(a) + (choices > kFewChoices ? choices * a.H * 4 : 0);
 }
 
 hipError_t launch_moe_layer(const LayerArgs &args, void *workspace, hipStream_t stream)
@@ -441,6 +577,7 @@ hipError_t launch_moe_layer(const LayerArgs &args, void *workspace, hipStream_t 
     LayerArgs a = args;
     a.table = workspace;
     a.h = static_cast<uint8_t *>(workspace) + sizeof(LayerTable);
+    a.rows = reinterpret_cast<float *>(static_cast<uint8_t *>(a.h) + h_bytes(a));
     if (a.e4m3)
         return a.bf16 ? launch<true, kWE4m3>(a, stream) : launch<false, kWE4m3>(a, stream);
     return a.bf16 ? launch<true, kW16>(a, stream) : launch<false, kW16>(a, stream);
