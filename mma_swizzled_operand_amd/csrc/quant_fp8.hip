@@ -35,12 +35,13 @@ __device__ __forceinline__ float max16(float v)
     return fmaxf(v, ror(v, std::integral_constant<int, 1>{}));
 }
 
-// The scale of a block whose largest magnitude is `most` (infinite if a value
-// is): most / 448, or the smallest power of two that is not below it.  A block
-// of zeros, or of values below 2^-90, takes 2^-90 as its largest.
+// What a block counts as its largest magnitude.
+__device__ __forceinline__ float largest(float most) { return fmaxf(most, 0x1p-90f); }
+
+// The scale of a block of that largest magnitude (infinite if a value is):
+// most / 448, or the smallest power of two that is not below it.
 __device__ __forceinline__ float scale_of(float most, bool pow2)
 {
-    most = fmaxf(most, 0x1p-90f);
     if (!pow2)
         return most / 448.0f;
     // 448 = 1.75 * 2^8: a mantissa up to 1.75 needs exponent - 8, above - 7
@@ -50,25 +51,45 @@ __device__ __forceinline__ float scale_of(float most, bool pow2)
     return __builtin_bit_cast(float, ((bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u)) << 23);
 }
 
-// What a block's values are divided with: 1 / s in two parts, so that the
-// quotient comes out within (1/2 + 2^-20) ulp.
+// What the values of a block are divided with: 1 / s in two parts, so that
+// x hi + x lo is within (1/2 + 2^-20) ulp of x / s and x / s itself where that is
+// a value of fp32.  The result need not be the quotient: it has to lie on the
+// quotient's side of every midpoint between two E4M3 values (five significant
+// bits at most), or on it.
+//
+// 16-bit x (p = 8 or 11 bits).  x, the block's largest A and a midpoint m are
+// integers X < 2^p, A < 2^p, u < 2^5 times powers of two, so x / (A / 448) either
+// is m, or 7 X 2^i and u A 2^j differ by one at least, i.e. by 2^-16 of
+// themselves.  s is A / 448 within 2^-24, so only in the first case can x / s be
+// close to m, and then it lies above or below as s was rounded down or up: the
+// same way for all of a block, which the lower part of 1 / s takes in with a
+// step of 2^-20.  (s exact, or a power of two: no step, and the quotient comes
+// out exactly.)
+//
+// fp32 x.  te, the sum with its last bit cleared, is within 1.5 ulp of x / s, so
+// it lies on the same side of every midpoint or on it.  The sign of the exact
+// remainder x - te s then moves it one ulp towards x / s, off the midpoint and
+// not as far as the next one.
+template <int IN>
 struct Divisor {
-    float s, hi, lo;
-    __device__ explicit Divisor(float scale) : s(scale)
+    float hi, lo, s;   // (s: fp32 x only)
+
+    __device__ Divisor() {}
+    __device__ Divisor(float scale, float most, bool pow2) : s(scale)
     {
         hi = 1.0f / s;
         // an infinite scale: finite values give 0, infinite ones NaN
         lo = hi == 0.0f ? 0.0f : fmaf(-s, hi, 1.0f) * hi;
+        if (IN != kOutF32 && !pow2) {
+            const float over = fmaf(s, 448.0f, -most);   // (the sign is exact)
+            lo += over > 0.0f ? hi * -0x1p-20f : over < 0.0f ? hi * 0x1p-20f : 0.0f;
+        }
     }
-    // A value that rounds to E4M3 as x / s does.  E4M3's values and the
-    // midpoints between them have at most five significant bits; te, the
-    // quotient with its last bit cleared, is within 1.5 ulp of x / s, so it
-    // lies on the same side of every midpoint or on it.  The sign of the
-    // exact remainder x - te s then moves it one ulp towards x / s, off the
-    // midpoint and not as far as the next one.
     __device__ float operator()(float x) const
     {
         const float t = fmaf(x, hi, x * lo);
+        if constexpr (IN != kOutF32)
+            return t;
         const float te = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, t) & ~1u);
         const float r = fmaf(-te, s, x);
         const float step = te * 0x1.8p-24f;
@@ -89,7 +110,10 @@ quant_fp8_kernel(const void *__restrict__ X, uint8_t *__restrict__ Q, float *__r
 {
     using T = std::conditional_t<IN == kOutF32, float, std::conditional_t<IN == kOutBf16, __bf16, _Float16>>;
     typedef T t8 __attribute__((ext_vector_type(8)));
-    __shared__ float most[4][128];
+    // the largest of each row, and of each column by wave; then the rows' and the
+    // columns' divisors
+    __shared__ float most[5][128];
+    __shared__ Divisor<IN> divisors[2][128];
     __shared__ __attribute__((aligned(16))) uint8_t turned[128 * 144];   // [column][row], rows of 144 bytes
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -117,6 +141,7 @@ quant_fp8_kernel(const void *__restrict__ X, uint8_t *__restrict__ Q, float *__r
         }
     }
     const int Mp = (M + 15) & ~15, blocks_m = (M + 127) / 128;
+    Divisor<IN> by_row[8], by_col[8];
     if constexpr (TILE) {
         float all = 0.0f;
 #pragma unroll
@@ -126,7 +151,7 @@ quant_fp8_kernel(const void *__restrict__ X, uint8_t *__restrict__ Q, float *__r
         if (cg == 0)
             most[0][rg] = all;
         __syncthreads();
-        all = max16(most[0][lane & 15]);
+        all = largest(max16(most[0][lane & 15]));
         const float s = scale_of(all, pow2);
         if (tid == 0) {
             if (Q)
@@ -134,39 +159,44 @@ quant_fp8_kernel(const void *__restrict__ X, uint8_t *__restrict__ Q, float *__r
             if (QT)
                 ST[int64_t(tk) * blocks_m + tm] = s;
         }
+        by_row[0] = Divisor<IN>(s, all, pow2);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            row_most[i] = col_most[i] = s;   // the scales, below
+            by_row[i] = by_col[i] = by_row[0];
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            row_most[i] = scale_of(max16(row_most[i]), pow2);
-            if (Q && cg == 0 && m + i < M)
-                S[int64_t(tk) * M + m + i] = row_most[i];
+            const float v = max16(row_most[i]);
+            if (cg == 0)
+                most[4][8 * rg + i] = v;
+            float c = col_most[i];
+            c = fmaxf(c, __shfl_xor(c, 16));
+            c = fmaxf(c, __shfl_xor(c, 32));
+            if (lane < 16)
+                most[wave][8 * cg + i] = c;
         }
-        if (QT) {
+        __syncthreads();
+        // one row or column a thread
+        const int at = tid & 127;
+        const bool col = tid >= 128;
+        const float v = largest(col ? fmaxf(fmaxf(most[0][at], most[1][at]), fmaxf(most[2][at], most[3][at])) : most[4][at]);
+        const float s = scale_of(v, pow2);
+        divisors[col][at] = Divisor<IN>(s, v, pow2);
+        if (!col && Q && m0 + at < M)
+            S[int64_t(tk) * M + m0 + at] = s;
+        if (col && QT && k0 + at < K)
+            ST[int64_t(tm) * K + k0 + at] = s;
+        __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float v = col_most[j];
-                v = fmaxf(v, __shfl_xor(v, 16));
-                v = fmaxf(v, __shfl_xor(v, 32));
-                if (lane < 16)
-                    most[wave][8 * cg + j] = v;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = 8 * cg + j;
-                col_most[j] = scale_of(fmaxf(fmaxf(most[0][c], most[1][c]), fmaxf(most[2][c], most[3][c])), pow2);
-                if (rg == 0 && in_k)
-                    ST[int64_t(tm) * K + k + j] = col_most[j];
-            }
+        for (int i = 0; i < 8; ++i) {
+            by_row[i] = divisors[0][8 * rg + i];
+            by_col[i] = divisors[1][8 * cg + i];
         }
     }
     if (Q) {
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            const Divisor by(row_most[r]);
+            const Divisor<IN> by = by_row[r];
             u32x2 q;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -179,7 +209,7 @@ quant_fp8_kernel(const void *__restrict__ X, uint8_t *__restrict__ Q, float *__r
     if (QT) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const Divisor by(col_most[j]);
+            const Divisor<IN> by = by_col[j];
             u32x2 q;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
