@@ -34,19 +34,21 @@
 namespace mswz {
 namespace {
 
-constexpr int kDownWaves = 8, kWaves = 4, kThreads = 64 * kWaves, kPerWave = kLayerChoices / kWaves;
+constexpr int kFewWaves = 8, kWaves = 4, kThreads = 64 * kWaves, kPerWave = kLayerChoices / kWaves;
 constexpr int kCols = 16;         // columns of h or y a workgroup
 constexpr int kFewChoices = 16;   // choices whose sums meet in LDS (one tile of tokens)
 
 enum Weights { kW16 = 0, kWE4m3 = 1 };
 
-// Where the second kernel finds the choices: experts in use, and all choices
-// sorted by expert (written by the first kernel).
+// Where the second kernel finds the choices (written by the first kernel): the
+// experts in use, one after the other, and all choices sorted by expert; one
+// read deep.
 struct LayerTable {
-    int32_t active;                      // experts with a choice
-    int32_t pad[3];
-    int32_t expert[1024], start[1024], count[1024];
-    int32_t order[kLayerChoices];
+    struct {
+        int32_t expert, start, count, pad;   // expert -1: no more in use
+    } slot[1024];
+    int32_t few[kFewChoices][kFewChoices];   // up to 16 choices: those of each slot, -1 behind the last
+    int32_t order[kLayerChoices];            // more: from the slot's start on
 };
 
 __device__ __forceinline__ float activation(float v, int act)
@@ -280,11 +282,10 @@ moe_layer_up_kernel(LayerArgs a, int parts)
             atomicOr(&used[id[i] >> 5], 1u << (id[i] & 31));
     }
     __syncthreads();
-    int expert = -1, active = 0;
+    int expert = -1;
     {
         const uint32_t word = lane < 32 ? used[lane] : 0u;
         const int n = __builtin_popcount(word), sum = wave_scan(n, lane);
-        active = __builtin_amdgcn_readlane(sum, 63);
         const int want = blockIdx.y;
         const uint64_t past = __ballot(sum > want);
         if (past) {
@@ -296,10 +297,11 @@ moe_layer_up_kernel(LayerArgs a, int parts)
         }
     }
     LayerTable *const table = static_cast<LayerTable *>(a.table);
-    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0)
-        table->active = active;
-    if (expert < 0)
+    if (expert < 0) {
+        if (blockIdx.x == 0 && tid == 0)
+            table->slot[blockIdx.y].expert = -1;
         return;
+    }
     int mine = 0, below = 0;
 #pragma unroll
     for (int i = 0; i < kPerWave / 64; ++i) {
@@ -326,12 +328,17 @@ moe_layer_up_kernel(LayerArgs a, int parts)
     }
     __syncthreads();
     if (blockIdx.x == 0) {
-        for (int r = tid; r < n; r += kThreads)
-            table->order[start + r] = rows[r];
+        if (choices <= kFewChoices) {
+            if (tid < kFewChoices)
+                table->few[blockIdx.y][tid] = tid < n ? rows[tid] : -1;
+        } else {
+            for (int r = tid; r < n; r += kThreads)
+                table->order[start + r] = rows[r];
+        }
         if (tid == 0) {
-            table->expert[blockIdx.y] = expert;
-            table->start[blockIdx.y] = start;
-            table->count[blockIdx.y] = n;
+            table->slot[blockIdx.y].expert = expert;
+            table->slot[blockIdx.y].start = start;
+            table->slot[blockIdx.y].count = n;
         }
     }
 
@@ -426,42 +433,44 @@ down_stream(const LayerArgs &a, int expert, int h0, const int *choice, int x16)
 // choice's sums go to LDS and a token's are added up in the order of its
 // choices.
 template <bool BF16, int WK>
-__global__ void __launch_bounds__(64 * kDownWaves)
-moe_layer_down_kernel(LayerArgs a, int splits)
+__global__ void __launch_bounds__(64 * kFewWaves)
+moe_layer_down_kernel(LayerArgs a, int slots, int splits)
 {
-    __shared__ __attribute__((aligned(16))) float of_choice[kDownWaves * kFewChoices * kCols];   // [splits][choices][16]
+    __shared__ __attribute__((aligned(16))) float of_choice[kFewWaves * kFewChoices * kCols];   // [splits][choices][16]
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int choices = a.T * a.topk;
+    const int choices = a.T * a.topk, h0 = blockIdx.x * kCols, x16 = lane & 15, g = lane >> 4, split = wave % splits;
     const LayerTable *const table = static_cast<const LayerTable *>(a.table);
-    const int active = table->active;
-    const int h0 = blockIdx.x * kCols, x16 = lane & 15, g = lane >> 4, split = wave % splits;
+    // lane c: choice c's expert and weight, for the sums below
+    const int id = lane < choices ? a.ids[lane] : -1;
+    const float weight = lane < choices ? a.w[lane] : 0.0f;
     int u0, u1;
     share<WK>(uint32_t(a.I) * (WK == kWE4m3 ? 1 : 2), split, splits, u0, u1);
-    for (int slot = wave / splits; slot < active; slot += kDownWaves / splits) {
-        const int n = table->count[slot];   // (at most kFewChoices, 16)
-        const int choice = x16 < n ? table->order[table->start[slot] + x16] : -1;
-        auto s = down_stream<BF16, WK, 1, 1, 4>(a, table->expert[slot], h0, &choice, x16);
+    for (int slot = wave / splits; slot < slots; slot += kFewWaves / splits) {
+        const int choice = table->few[slot][x16], expert = table->slot[slot].expert;
+        if (expert < 0)
+            break;
+        auto s = down_stream<BF16, WK, 1, 1, 4>(a, expert, h0, &choice, x16);
         s.run(u0, u1, blockIdx.x, g);
         if (choice >= 0)
             *reinterpret_cast<f32x4 *>(of_choice + (split * choices + choice) * kCols + 4 * g) = s.acc[0][0];
     }
     __syncthreads();
     using T = std::conditional_t<BF16, __bf16, _Float16>;
-    for (int o = tid; o < a.T * kCols; o += 64 * kDownWaves) {
-        const int t = o / kCols, col = o % kCols;
-        float y = 0.0f;
-        for (int j = 0; j < a.topk; ++j) {
-            const int c = t * a.topk + j;
-            if (uint32_t(a.ids[c]) >= uint32_t(a.E))
-                continue;
-            float v = 0.0f;
-            for (int s = 0; s < splits; ++s)
-                v += of_choice[(s * choices + c) * kCols + col];
-            y = fmaf(a.w[c], v, y);
-        }
-        if (h0 + col < a.H)
-            static_cast<T *>(a.Y)[int64_t(t) * a.ldx + h0 + col] = T(y);
+    const int t = tid / kCols, col = tid % kCols;   // (at most 16 tokens of 16 columns)
+    if (wave >= (kFewChoices * kCols) / 64)
+        return;
+    float y = 0.0f;
+    for (int j = 0; j < a.topk; ++j) {
+        const int c = min(t, a.T - 1) * a.topk + j;
+        const float w = __shfl(weight, c);
+        const bool in = uint32_t(__shfl(id, c)) < uint32_t(a.E);
+        float v = 0.0f;
+        for (int s = 0; s < splits; ++s)
+            v += in ? of_choice[(s * choices + c) * kCols + col] : 0.0f;
+        y = in ? fmaf(w, v, y) : y;
     }
+    if (t < a.T && h0 + col < a.H)
+        static_cast<T *>(a.Y)[int64_t(t) * a.ldx + h0 + col] = T(y);
 }
 
 // The second kernel for more choices: those of one expert, in fp32 rows of the
@@ -474,9 +483,9 @@ moe_layer_rows_kernel(LayerArgs a, int parts)
     __shared__ __attribute__((aligned(16))) f32x4 sums[kWaves][TILES][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const LayerTable *const table = static_cast<const LayerTable *>(a.table);
-    if (int(blockIdx.y) >= table->active)
+    const int expert = table->slot[blockIdx.y].expert, start = table->slot[blockIdx.y].start, n = table->slot[blockIdx.y].count;
+    if (expert < 0)
         return;
-    const int expert = table->expert[blockIdx.y], start = table->start[blockIdx.y], n = table->count[blockIdx.y];
     const int h0 = (int(blockIdx.x) * (kWaves / parts) + wave / parts) * TILES * kCols, x16 = lane & 15, g = lane >> 4;
     int u0, u1;
     share<WK>(uint32_t(a.I) * (WK == kWE4m3 ? 1 : 2), wave % parts, parts, u0, u1);
@@ -548,11 +557,12 @@ hipError_t launch(const LayerArgs &a, hipStream_t stream)
     const int slabs = (a.I + 8 * TILES - 1) / (8 * TILES), parts = parts_for(slabs);
     hipLaunchKernelGGL((moe_layer_up_kernel<BF16, WK>), dim3(groups(slabs, parts), experts), block, 0, stream, a, parts);
     if (choices <= kFewChoices) {
-        // waves that share an expert, until the experts in use can be as many as waves
+        // waves that share an expert, as long as there is one for each
         int splits = 1;
-        while (splits < kDownWaves && experts * splits < kDownWaves)
+        while (2 * splits * experts <= kFewWaves)
             splits *= 2;
-        hipLaunchKernelGGL((moe_layer_down_kernel<BF16, WK>), dim3((a.H + kCols - 1) / kCols), dim3(64 * kDownWaves), 0, stream, a, splits);
+        hipLaunchKernelGGL((moe_layer_down_kernel<BF16, WK>), dim3((a.H + kCols - 1) / kCols), dim3(64 * kFewWaves), 0, stream,
+                           a, experts, splits);
     } else {
         const int wide = (a.H + TILES * kCols - 1) / (TILES * kCols), shared = parts_for(wide);
         hipLaunchKernelGGL((moe_layer_rows_kernel<BF16, WK>), dim3(groups(wide, shared), experts), block, 0, stream, a, shared);
