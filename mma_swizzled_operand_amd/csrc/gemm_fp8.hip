@@ -22,14 +22,15 @@ bool is_skinny(const Fp8Args &a) { return a.M <= 32 && tiles(a, 64, 64) < (a.M >
 
 // K parts of a product: where tiles of 64 x 64 leave half of the compute units
 // idle and K is long, it is split until there are as many, each part keeping
-// eight blocks at least (four and twelve: within 3 %).  Unsplit and split: 64 x
-// 2048 x 8192 21.0 and 12.4 us, 64 x 4096 x 4096 12.5 and 10.9, 128 x 4096 x 8192
-// 23.8 and 18.8; with fewer than 24 blocks the second launch takes what the
-// split gives.
+// eight blocks at least (four and twelve: within 3 %).  Unsplit, with tiles of 32
+// x 64, and split: 64 x 2048 x 8192 16.6 and 12.2 us, 512 x 512 x 8192 16.4 and
+// 13.4, 128 x 4096 x 8192 19.7 and 18.8; 64 x 4096 x 4096 10.2 and 11.8, 100 x 1000
+// x 4096 9.8 and 10.9: with few blocks the second launch takes what the split
+// gives.
 int parts_of(const Fp8Args &a)
 {
     const int64_t t = tiles(a, 64, 64);
-    if (is_skinny(a) || t > 128 || a.kb < 24)
+    if (is_skinny(a) || t > 128 || a.kb < 48)
         return 1;
     const int64_t most = a.kb / 8;
     return int(256 / t < most ? 256 / t : most);
@@ -73,27 +74,30 @@ hipError_t launch_out(const Fp8Args &a, hipStream_t stream)
     // The tile whose rounds over the chip take the least time.  A tile's time,
     // in units of 10 ns for one block of K, is what one round took (K 4096, 16-bit
     // D); the compute units hold one workgroup each but for the tile of 128 x 128
-    // by four waves, of which they hold two.  (4096 x 4096 x 4096: 137, 125, 97, 88
-    // and 67 us in this order; 256 x 4096 x 4096: 13.7, 18, 23, 31, 56; 1024 x 4096
-    // x 4096: 38, 35, 25, 34, 57; 4096 x 2048 x 4096: 68, 66, 49, 45, 59.)  The
-    // largest does not leave the bf16 form registers, so an fp32 D stops at 128
-    // x 128 (4096 x 4096 x 4096 147 us, 238 with it).
+    // by four waves, of which they hold two.  (From 64 x 64 on, 4096 x 4096 x 4096:
+    // 137, 125, 97, 88 and 67 us; 256 x 4096 x 4096: 13.7, 18, 23, 31, 56, and 16.9
+    // with 32 x 64; 128 x 4096 x 4096: 12.9, 17, 23, 31, 48, and 11.0; 1024 x 4096 x
+    // 4096: 38, 35, 25, 34, 57; 4096 x 2048 x 4096: 68, 66, 49, 45, 59.)  The largest
+    // does not leave the bf16 form registers, so an fp32 D stops at 128 x 128
+    // (4096 x 4096 x 4096 147 us, 238 with it).
     const struct {
         int64_t rounds, time;
-    } all[5] = {{(tiles(a, 64, 64) + 255) / 256, 25},
+    } all[6] = {{(tiles(a, 32, 64) + 255) / 256, 17},
+                {(tiles(a, 64, 64) + 255) / 256, 25},
                 {(tiles(a, 128, 64) + 255) / 256, 42},
                 {(tiles(a, 128, 128) + 255) / 256, 72},
                 {(tiles(a, 128, 128) + 511) / 512, 123},
                 {(tiles(a, 256, 256) + 255) / 256, 200}};
     int best = 0;
-    for (int i = 1; i < (OUT == kOutF32 ? 4 : 5); ++i)
+    for (int i = 1; i < (OUT == kOutF32 ? 5 : 6); ++i)
         if (all[i].rounds * all[i].time <= all[best].rounds * all[best].time)
             best = i;
     switch (best) {
-    case 0: return launch_tile<64, 64, 32, 32, 4, ROWB, OUT>(a, stream);
-    case 1: return launch_tile<128, 64, 32, 32, 4, ROWB, OUT>(a, stream);
-    case 2: return launch_tile<128, 128, 64, 32, 4, ROWB, OUT>(a, stream);
-    case 3: return launch_tile<128, 128, 64, 64, 2, ROWB, OUT>(a, stream);
+    case 0: return launch_tile<32, 64, 16, 32, 4, ROWB, OUT>(a, stream);
+    case 1: return launch_tile<64, 64, 32, 32, 4, ROWB, OUT>(a, stream);
+    case 2: return launch_tile<128, 64, 32, 32, 4, ROWB, OUT>(a, stream);
+    case 3: return launch_tile<128, 128, 64, 32, 4, ROWB, OUT>(a, stream);
+    case 4: return launch_tile<128, 128, 64, 64, 2, ROWB, OUT>(a, stream);
     }
     if constexpr (OUT != kOutF32)
         return launch_tile<256, 256, 128, 64, 2, ROWB, OUT>(a, stream);

@@ -135,7 +135,7 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
     constexpr int W = (BM / WM) * (BN / WN), TI = WM / 16, TJ = WN / 16;
     constexpr int kAB = (BM + BN) * 128;
     // scale words of a step: wave w copies 64 of them into slot w of the stage
-    constexpr int kSlotsA = BM / 64, kSlotsB = ROWB ? BN / 64 : 1;
+    constexpr int kSlotsA = (BM + 63) / 64, kSlotsB = ROWB ? (BN + 63) / 64 : 1;
     static_assert(kSlotsA + kSlotsB <= W, "one instruction a wave");
     // (arrays of their own: reads of one stage do not wait for copies into another)
     __shared__ __attribute__((aligned(1024))) uint8_t lds0[kAB];
@@ -146,7 +146,6 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
     __shared__ __attribute__((aligned(256))) uint8_t scl1[256 * W];
     __shared__ __attribute__((aligned(256))) uint8_t scl2[S > 2 ? 256 * W : 16];
     __shared__ __attribute__((aligned(256))) uint8_t scl3[S > 3 ? 256 * W : 16];
-
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     auto stage = [&](auto n) { return std::get<decltype(n)::value>(std::make_tuple(lds0, lds1, lds2, lds3)); };
     auto scales_of = [&](auto n) { return std::get<decltype(n)::value>(std::make_tuple(scl0, scl1, scl2, scl3)); };
@@ -255,7 +254,8 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
         });
     };
     // a step ends when the next one's copies are in LDS; those of the S - 2
-    // steps after it stay in flight
+    // steps after it stay in flight (six and eight stages of 64 x 64: 64 x 16384 x
+    // 8192 38 us, 35 with four)
     constexpr int kCopies = decltype(ca)::kInstr + decltype(cb)::kInstr + 1;
     auto step_end = [] {
         __builtin_amdgcn_sched_barrier(0);
