@@ -58,7 +58,7 @@ hipError_t launch_tile(const Fp8Args &a, hipStream_t stream, int parts = 1)
     parts = (a.kb + per - 1) / per;
     hipLaunchKernelGGL((gemm_fp8_kernel<BM, BN, WM, WN, S, ROWB, OUT == kOutF32, OUT>),
                        dim3(uint32_t(tiles_m) * uint32_t(tiles_n), parts), dim3(64 * (BM / WM) * (BN / WN)), 0, stream, a,
-                       tiles_m, tiles_n, -4, per, fp8_whole_stores(a));
+                       tiles_m, tiles_n, -4, per, parts == 1 && fp8_whole_lines(a) ? 2 : int(fp8_whole_stores(a)));
     if (parts > 1)
         hipLaunchKernelGGL(fp8_reduce_kernel, dim3(uint32_t((fp8_part_pitch(a.N) / 4 * a.M + 255) / 256)), dim3(256), 0,
                            stream, a, parts, fp8_whole_stores(a));

@@ -86,6 +86,13 @@ inline bool fp8_whole_stores(const Fp8Args &a)
     return a.ldd % 4 == 0 && (reinterpret_cast<uintptr_t>(a.D) & (a.out == kOutF32 ? 15 : 7)) == 0;
 }
 
+// Whether a 16-bit D without an old one is made of whole, aligned pieces of 16
+// bytes.
+inline bool fp8_whole_lines(const Fp8Args &a)
+{
+    return a.out != kOutF32 && !a.beta && a.N % 8 == 0 && a.ldd % 8 == 0 && (reinterpret_cast<uintptr_t>(a.D) & 15) == 0;
+}
+
 // The LDS tile's layout: rows of 128 bytes, 16-byte chunk c of row r at place
 // c ^ fp8_key(r).  As layout.hpp's tile_key for the rows of one fragment, but
 // the same for every 16 rows: all fragments of an operand are read from two
@@ -130,7 +137,7 @@ struct Fp8Copy {
 // rows (else to 128 x 128 tiles).  EXACT: by way of bf16.  OUT: D's kind.
 template <int BM, int BN, int WM, int WN, int S, bool ROWB, bool EXACT, int OUT>
 __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN))
-gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_part, bool vec)
+gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_part, int vec)
 {
     constexpr int W = (BM / WM) * (BN / WN), TI = WM / 16, TJ = WN / 16;
     constexpr int kAB = (BM + BN) * 128;
@@ -275,6 +282,38 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
         });
     lds_barrier_keep_vm<0>();   // no copy may still be writing LDS when the workgroup ends
 
+    // 16-bit D, 64 columns a wave: the tile goes through LDS (16-byte chunk c of
+    // row r at place c ^ (r % 8) of its 128 bytes) and out as whole lines past the
+    // caches, as long as every piece of 16 bytes is aligned
+    if constexpr (OUT != kOutF32 && WN == 64) {
+        static_assert(BM * BN * 2 <= 2 * kAB && (BM * BN * 2 <= kAB || W % 2 == 0), "in two stages");
+        if (vec == 2) {
+            using T = std::conditional_t<OUT == kOutBf16, __bf16, _Float16>;
+            typedef T t4 __attribute__((ext_vector_type(4)));
+            typedef T t8 __attribute__((ext_vector_type(8)));
+            constexpr int kMine = WM * 128, kFit = kAB / kMine;   // waves whose tiles one stage holds
+            uint8_t *const mine = (wave < kFit ? lds0 : lds1) + wave % kFit * kMine;
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int j = 0; j < TJ; ++j) {
+                    const uint32_t r = 16 * i + x16, c = 2 * j + (g >> 1);
+                    *reinterpret_cast<t4 *>(mine + r * 128 + ((c ^ (r & 7)) << 4) + 8 * (g & 1)) =
+                        t4{T(acc[j][i][0]), T(acc[j][i][1]), T(acc[j][i][2]), T(acc[j][i][3])};
+                }
+            wave_lds_sync();
+            const int n = n0 + wn + 8 * (lane & 7);
+#pragma unroll 4
+            for (int k = 0; k < WM / 8; ++k) {
+                const uint32_t r = 8 * k + (lane >> 3);
+                const int m = m0 + wm + int(r);
+                if (m < a.M && n < a.N)
+                    __builtin_nontemporal_store(*reinterpret_cast<const t8 *>(mine + r * 128 + (((lane & 7) ^ (r & 7)) << 4)),
+                                                reinterpret_cast<t8 *>(static_cast<T *>(a.D) + int64_t(m) * a.ldd + n));
+            }
+            return;
+        }
+    }
     // a part of K leaves its sums in the workspace, in rows of whole 16-byte pieces
     const bool split = gridDim.y > 1;
     const int64_t pitch = fp8_part_pitch(a.N);
@@ -291,7 +330,7 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
                 if (n < a.N)
                     *reinterpret_cast<f32x4 *>(part + m * pitch + n) = acc[j][i];
             } else {
-                fp8_store_as<OUT>(a, m, n, acc[j][i], vec);
+                fp8_store_as<OUT>(a, m, n, acc[j][i], vec != 0);
             }
         }
     }
