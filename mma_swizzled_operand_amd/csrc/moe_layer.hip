@@ -158,12 +158,27 @@ struct Stream {
     {
         if constexpr (!DOWN)
             return mfma_16x16x32<BF16>(w, x[0], c);
-        else if constexpr (BF16 || WK == kWE4m3)
+        else
             return mfma_16x16x32<true>(w, x[1], mfma_16x16x32<true>(w, x[0], c));
-        u32x4 hi, lo;
-        split_f16x8(w, hi, lo);
-        c = mfma_16x16x32<true>(hi, x[1], mfma_16x16x32<true>(hi, x[0], c));
-        return mfma_16x16x32<true>(lo, x[1], mfma_16x16x32<true>(lo, x[0], c));
+    }
+
+    // the same for all tiles of tokens (fp16 weights are split once for them)
+    template <int N>
+    static __device__ __forceinline__ void steps(u32x4 w, const u32x4 (*x)[NX], f32x4 (*sum)[TILES], int tile)
+    {
+        if constexpr (DOWN && !BF16) {
+            u32x4 hi, lo;
+            split_f16x8(w, hi, lo);
+#pragma unroll
+            for (int t = 0; t < N; ++t) {
+                sum[t][tile] = mfma_16x16x32<true>(hi, x[t][1], mfma_16x16x32<true>(hi, x[t][0], sum[t][tile]));
+                sum[t][tile] = mfma_16x16x32<true>(lo, x[t][1], mfma_16x16x32<true>(lo, x[t][0], sum[t][tile]));
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < N; ++t)
+                sum[t][tile] = step(w, x[t], sum[t][tile]);
+        }
     }
 
     // units u0 .. u1 - 1 (E4M3: both even), the turn-th and the ones after it
@@ -191,9 +206,7 @@ struct Stream {
 #pragma unroll
                 for (int w = 0; w < TILES; ++w) {
                     if constexpr (WK == kW16) {
-#pragma unroll
-                        for (int t = 0; t < NT; ++t)
-                            acc[t][w] = step(d[i].w[w], d[i].x[t], acc[t][w]);
+                        steps<NT>(d[i].w[w], d[i].x, acc, w);
                     } else {
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
@@ -216,15 +229,17 @@ struct Stream {
     }
 };
 
-// Calls fn with one or two tiles of 16 rows at a time, rows r0 .. of n.
-template <class Fn>
+// Calls fn with up to MOST (2 or 4) tiles of 16 rows at a time, rows r0 .. of n.
+template <int MOST, class Fn>
 __device__ __forceinline__ void by_rows(int n, Fn &&fn)
 {
-    for (int r0 = 0; r0 < n; r0 += 32)
+    for (int r0 = 0; r0 < n; r0 += 16 * MOST)
         if (n - r0 <= 16)
             fn(r0, std::integral_constant<int, 1>{});
-        else
+        else if (MOST == 2 || n - r0 <= 32)
             fn(r0, std::integral_constant<int, 2>{});
+        else
+            fn(r0, std::integral_constant<int, MOST>{});
 }
 
 // The sums of the `parts` waves that share a product, one tile of tokens: the
@@ -256,20 +271,22 @@ __device__ __forceinline__ void share(uint32_t row_bytes, int part, int parts, i
     u1 = per * (units * (part + 1) / parts);
 }
 
-// The first kernel: the choices of one expert, the blockIdx.y-th of those in
-// use; 8 * TILES columns of h for every `parts` waves.
-template <bool BF16, int WK>
-__global__ void __launch_bounds__(kThreads)
-moe_layer_up_kernel(LayerArgs a, int parts)
-{
-    __shared__ uint32_t used[32];
-    __shared__ int before[2][kWaves];
-    __shared__ uint16_t rows[kLayerChoices];
-    __shared__ __attribute__((aligned(16))) f32x4 sums[kWaves][tiles_of<WK>()][64];
+// The blockIdx.y-th of the experts in use (-1: there are fewer) and its n
+// choices, in ascending order, in LDS; the first workgroup of an expert writes
+// them down for the second kernel.
+struct ExpertRows {
+    uint32_t used[32];
+    int before[2][kWaves];
+    uint16_t rows[kLayerChoices];
+};
 
+__device__ __forceinline__ int find_expert(const LayerArgs &a, ExpertRows &lds, int &n)
+{
+    uint32_t *const used = lds.used;
+    int(*const before)[kWaves] = lds.before;
+    uint16_t *const rows = lds.rows;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int choices = a.T * a.topk;
-    // ---- the expert and its choices, in ascending order ----
     if (tid < 32)
         used[tid] = 0;
     __syncthreads();
@@ -300,7 +317,7 @@ moe_layer_up_kernel(LayerArgs a, int parts)
     if (expert < 0) {
         if (blockIdx.x == 0 && tid == 0)
             table->slot[blockIdx.y].expert = -1;
-        return;
+        return -1;
     }
     int mine = 0, below = 0;
 #pragma unroll
@@ -313,7 +330,8 @@ moe_layer_up_kernel(LayerArgs a, int parts)
         before[1][wave] = below;
     }
     __syncthreads();
-    int n = 0, start = 0, at = 0;
+    int start = 0, at = 0;
+    n = 0;
     for (int w = 0; w < kWaves; ++w) {
         at += w < wave ? before[0][w] : 0;
         n += before[0][w];
@@ -341,40 +359,79 @@ moe_layer_up_kernel(LayerArgs a, int parts)
             table->slot[blockIdx.y].count = n;
         }
     }
+    return expert;
+}
 
-    // ---- the products ----
+// Four columns i .. i + 3 of a choice's h from the two sums.
+__device__ __forceinline__ void store_h(const LayerArgs &a, int choice, int i, f32x4 gate, f32x4 up)
+{
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        split_bf16(activation(gate[e], a.act) * up[e], hi[e], lo[e]);
+    // of every 8 columns the upper parts, then the lower ones
+    uint8_t *const to = static_cast<uint8_t *>(a.h) + (int64_t(choice) * a.I + (i & ~7)) * 4 + 2 * (i & 7);
+    *reinterpret_cast<u32x2 *>(to) = u32x2{hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16)};
+    *reinterpret_cast<u32x2 *>(to + 16) = u32x2{lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16)};
+}
+
+// What the first kernels share: TILES / 2 tiles of 16 columns of h from i0 on, the
+// gate's rows and the others in turn.
+template <bool BF16, int WK, int TILES, int NT, int kDepth>
+__device__ __forceinline__ Stream<BF16, WK, false, TILES, NT, kDepth>
+up_stream(const LayerArgs &a, int expert, int i0, int x16)
+{
+    const uint32_t row_bytes = uint32_t(a.H) * (WK == kWE4m3 ? 1 : 2);
+    const int ib = (a.I + 127) / 128, hb = (a.H + 127) / 128;
+    Stream<BF16, WK, false, TILES, NT, kDepth> s;
+    s.row_bytes = row_bytes;
+    s.w_end = 2u * uint32_t(a.I) * row_bytes;
+    s.w_rsrc = make_rsrc(static_cast<const uint8_t *>(a.W1) + uint64_t(expert) * s.w_end, s.w_end);
+    s.x_end = uint32_t(a.T - 1) * uint32_t(a.ldx) * 2 + uint32_t(a.H) * 2;
+    s.x_rsrc = make_rsrc(a.X, s.x_end);
+#pragma unroll
+    for (int c = 0; c < TILES / 2; ++c) {
+        s.w_row[2 * c] = uint32_t(min(i0 + 16 * c + x16, a.I - 1)) * row_bytes;
+        s.w_row[2 * c + 1] = s.w_row[2 * c] + uint32_t(a.I) * row_bytes;
+    }
+    if constexpr (WK == kWE4m3) {
+        s.s_end = 2u * uint32_t(ib) * uint32_t(hb) * 4;
+        s.s_rsrc = make_rsrc(a.S1 + int64_t(expert) * 2 * ib * hb, s.s_end);
+        s.s_row[0] = uint32_t(min(i0, a.I - 1) / 128) * uint32_t(hb) * 4;
+        s.s_row[1] = s.s_row[0] + uint32_t(ib) * uint32_t(hb) * 4;
+    }
+    return s;
+}
+
+// The first kernel: the choices of one expert, the blockIdx.y-th of those in
+// use; 8 * TILES columns of h for every `parts` waves.
+template <bool BF16, int WK>
+__global__ void __launch_bounds__(kThreads)
+moe_layer_up_kernel(LayerArgs a, int parts)
+{
+    __shared__ ExpertRows found;
+    __shared__ __attribute__((aligned(16))) f32x4 sums[kWaves][tiles_of<WK>()][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int n;
+    const int expert = find_expert(a, found, n);
+    if (expert < 0)
+        return;
+    const uint16_t *const rows = found.rows;
     constexpr int kSize = WK == kWE4m3 ? 1 : 2;
     constexpr int TILES = tiles_of<WK>();
     const int i0 = (int(blockIdx.x) * (kWaves / parts) + wave / parts) * (8 * TILES), x16 = lane & 15, g = lane >> 4;
     const uint32_t row_bytes = uint32_t(a.H) * kSize, x_pitch = uint32_t(a.ldx) * 2;
-    const int ib = (a.I + 127) / 128, hb = (a.H + 127) / 128;
     int u0, u1;
     share<WK>(row_bytes, wave % parts, parts, u0, u1);
     if (i0 >= a.I)
         u1 = u0;   // (this wave's columns lie behind the last)
-    by_rows(n, [&](int r0, auto tiles) {
+    by_rows<2>(n, [&](int r0, auto tiles) {
         constexpr int NT = decltype(tiles)::value;
-        Stream<BF16, WK, false, TILES, NT, depth_of<WK>(NT)> s;
-        s.row_bytes = row_bytes;
-        s.w_end = 2u * uint32_t(a.I) * row_bytes;
-        s.w_rsrc = make_rsrc(static_cast<const uint8_t *>(a.W1) + uint64_t(expert) * s.w_end, s.w_end);
-#pragma unroll
-        for (int c = 0; c < TILES / 2; ++c) {
-            s.w_row[2 * c] = uint32_t(min(i0 + 16 * c + x16, a.I - 1)) * row_bytes;
-            s.w_row[2 * c + 1] = s.w_row[2 * c] + uint32_t(a.I) * row_bytes;
-        }
-        s.x_end = uint32_t(a.T - 1) * x_pitch + uint32_t(a.H) * 2;
-        s.x_rsrc = make_rsrc(a.X, s.x_end);
+        auto s = up_stream<BF16, WK, TILES, NT, depth_of<WK>(NT)>(a, expert, i0, x16);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int r = r0 + 16 * t + x16;
             s.x_row[t] = r < n ? uint32_t(rows[r] / uint32_t(a.topk)) * x_pitch : s.x_end;
-        }
-        if constexpr (WK == kWE4m3) {
-            s.s_end = 2u * uint32_t(ib) * uint32_t(hb) * 4;
-            s.s_rsrc = make_rsrc(a.S1 + int64_t(expert) * 2 * ib * hb, s.s_end);
-            s.s_row[0] = uint32_t(min(i0, a.I - 1) / 128) * uint32_t(hb) * 4;
-            s.s_row[1] = s.s_row[0] + uint32_t(ib) * uint32_t(hb) * 4;
         }
         s.run(u0, u1, i0 / (8 * TILES), g);
 #pragma unroll
@@ -387,14 +444,7 @@ moe_layer_up_kernel(LayerArgs a, int parts)
                 const int i = i0 + 16 * c + 4 * g;
                 if (wave % parts != 0 || r >= n || i >= a.I)
                     continue;
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    split_bf16(activation(v[2 * c][e], a.act) * v[2 * c + 1][e], hi[e], lo[e]);
-                // of every 8 columns the upper parts, then the lower ones
-                uint8_t *const to = static_cast<uint8_t *>(a.h) + (int64_t(rows[r]) * a.I + (i & ~7)) * 4 + 2 * (i & 7);
-                *reinterpret_cast<u32x2 *>(to) = u32x2{hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16)};
-                *reinterpret_cast<u32x2 *>(to + 16) = u32x2{lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16)};
+                store_h(a, rows[r], i, v[2 * c], v[2 * c + 1]);
             }
         }
     });
@@ -491,7 +541,7 @@ moe_layer_rows_kernel(LayerArgs a, int parts)
     share<WK>(uint32_t(a.I) * (WK == kWE4m3 ? 1 : 2), wave % parts, parts, u0, u1);
     if (h0 >= a.H)
         u1 = u0;   // (this wave's columns lie behind the last)
-    by_rows(n, [&](int r0, auto tiles) {
+    by_rows<2>(n, [&](int r0, auto tiles) {
         constexpr int NT = decltype(tiles)::value;
         int choice[NT];
 #pragma unroll
@@ -508,6 +558,188 @@ moe_layer_rows_kernel(LayerArgs a, int parts)
                 for (int i = 0; i < TILES; ++i)
                     if (h0 + 16 * i + 4 * g < a.H)
                         *reinterpret_cast<f32x4 *>(a.rows + int64_t(choice[t]) * a.H + h0 + 16 * i + 4 * g) = v[i];
+        }
+    });
+}
+
+// As Stream, for many rows of tokens: a workgroup's four waves have weight rows
+// of their own and take the tokens' values from LDS, which direct copies fill a
+// chunk of kUnits units ahead, so that a token's row is read from the L2 once for
+// 128 weight rows.  Row r of a chunk has kChunk bytes, its 16-byte piece c at place
+// c ^ (r % 16).  The weights' loads are a chunk ahead in registers; a chunk's
+// barrier waits for the copies and leaves the loads behind them in flight.
+template <bool BF16, int WK, bool DOWN, int NT>
+struct Staged {
+    using One = Stream<BF16, WK, DOWN, 2, NT, 2>;
+    static constexpr int NX = One::NX, NS = One::NS, kUnits = NX == 4 ? 2 : 4, kChunk = 64 * NX * kUnits;
+    static constexpr int kInstr = NT * 16 * kChunk / 1024 / kWaves;
+    static constexpr int kLoads = 2 * kUnits + (WK == kWE4m3 ? NS * kUnits / 2 : 0);
+    struct Unit {
+        u32x4 w[2];
+        float s[NS];
+    };
+    uint32_t from[kInstr], at[kInstr];   // this lane's token row in each copy, and its place in a chunk
+
+    // row_of(r): byte offset of row r's values, x_end for none
+    template <class RowOf>
+    __device__ void init(RowOf &&row_of, int wave, int lane)
+    {
+#pragma unroll
+        for (int q = 0; q < kInstr; ++q) {
+            const int byte = 1024 * (wave + kWaves * q) + 16 * lane, r = byte / kChunk;
+            at[q] = 16 * uint32_t((byte % kChunk / 16) ^ (r & 15));
+            from[q] = row_of(r);
+        }
+    }
+    __device__ void copy(const One &o, uint8_t *stage, int chunk, uint32_t token_bytes, int wave) const
+    {
+#pragma unroll
+        for (int q = 0; q < kInstr; ++q) {
+            const uint32_t off = uint32_t(chunk) * kChunk + at[q];
+            buffer_load_lds16(o.x_rsrc, stage + 1024 * (wave + kWaves * q),
+                              off < token_bytes && from[q] != o.x_end ? from[q] + off : o.x_end, 0);
+        }
+    }
+    __device__ void load(const One &o, Unit &d, int u, int units, int g, bool last) const
+    {
+        const uint32_t off = 64u * uint32_t(u) + 16u * uint32_t(g);
+        const bool out = u >= units || off >= o.row_bytes;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            d.w[t] = buffer_load16(o.w_rsrc, out ? o.w_end : o.w_row[t] + off, 0);
+        if constexpr (WK == kWE4m3)
+            if (last)
+#pragma unroll
+                for (int t = 0; t < NS; ++t)
+                    d.s[t] = __builtin_bit_cast(float, buffer_load4(o.s_rsrc, u >= units ? o.s_end : o.s_row[t] + 4u * uint32_t(u / 2), 0));
+    }
+    // o: rows and ranges; its sums are the result
+    __device__ void run(One &o, uint8_t *stage0, uint8_t *stage1, uint32_t token_bytes, int wave, int lane) const
+    {
+        const int x16 = lane & 15, g = lane >> 4;
+        const int units = int((o.row_bytes + 63) / 64), whole = WK == kWE4m3 ? (units + 1) & ~1 : units;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            o.acc[t][0] = o.acc[t][1] = f32x4{};
+        Unit d[kUnits];
+        copy(o, stage0, 0, token_bytes, wave);
+        static_for<0, kUnits>([&](auto i) {
+            load(o, d[i], i, whole, g, i % 2 == 1);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        lds_barrier_keep_vm<kLoads>();
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 part[NT][2];
+        auto chunk = [&](const uint8_t *stage, uint8_t *next, int c) {
+            copy(o, next, c + 1, token_bytes, wave);
+            __builtin_amdgcn_sched_barrier(0);
+            static_for<0, kUnits>([&](auto ic) {
+                constexpr int i = decltype(ic)::value;
+                u32x4 x[NT][NX];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int p = 0; p < NX; ++p)
+                        x[t][p] = lds_read16(stage, (16 * t + x16) * kChunk + (((NX * (4 * i + g) + p) ^ x16) << 4));
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if constexpr (WK == kW16) {
+                        One::template steps<NT>(d[i].w[w], x, o.acc, w);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const u32x4 v = from_e4m3<BF16 || DOWN>(d[i].w[w][2 * q], d[i].w[w][2 * q + 1]);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+                                part[t][w] = One::step(v, x[t] + q * (NX / 2), i % 2 == 0 && q == 0 ? f32x4{} : part[t][w]);
+                        }
+                        if (i % 2 == 1)
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                for (int r = 0; r < 4; ++r)
+                                    o.acc[t][w][r] = fmaf(d[i].s[w % NS], part[t][w][r], o.acc[t][w][r]);
+                    }
+                }
+                load(o, d[i], (c + 1) * kUnits + i, whole, g, i % 2 == 1);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            lds_barrier_keep_vm<kLoads>();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        const int chunks = (whole + kUnits - 1) / kUnits;
+        for (int c = 0; c < chunks; c += 2) {
+            chunk(stage0, stage1, c);
+            if (c + 1 < chunks)
+                chunk(stage1, stage0, c + 1);
+        }
+        lds_barrier_keep_vm<0>();   // no copy may still be writing LDS
+    }
+};
+
+// The kernels of a layer with many choices for an expert: as moe_layer_up_kernel
+// and moe_layer_rows_kernel, 64 columns of h and 128 of y a workgroup.
+template <bool BF16, int WK>
+__global__ void __launch_bounds__(kThreads)
+moe_layer_up_staged_kernel(LayerArgs a)
+{
+    __shared__ ExpertRows found;
+    __shared__ __attribute__((aligned(1024))) uint8_t stage0[Staged<BF16, WK, false, 4>::kInstr * kWaves * 1024];
+    __shared__ __attribute__((aligned(1024))) uint8_t stage1[Staged<BF16, WK, false, 4>::kInstr * kWaves * 1024];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int n;
+    const int expert = find_expert(a, found, n);
+    if (expert < 0)
+        return;
+    const uint16_t *const rows = found.rows;
+    const int i0 = (int(blockIdx.x) * kWaves + wave) * kCols;
+    by_rows<4>(n, [&](int r0, auto tiles) {
+        constexpr int NT = decltype(tiles)::value;
+        auto o = up_stream<BF16, WK, 2, NT, 2>(a, expert, i0, lane & 15);
+        Staged<BF16, WK, false, NT> s;
+        s.init([&](int r) { return r0 + r < n ? uint32_t(rows[r0 + r] / uint32_t(a.topk)) * uint32_t(a.ldx) * 2 : o.x_end; },
+               wave, lane);
+        s.run(o, stage0, stage1, uint32_t(a.H) * 2, wave, lane);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int r = r0 + 16 * t + (lane & 15), i = i0 + 4 * (lane >> 4);
+            if (r < n && i < a.I)
+                store_h(a, rows[r], i, o.acc[t][0], o.acc[t][1]);
+        }
+    });
+}
+
+template <bool BF16, int WK>
+__global__ void __launch_bounds__(kThreads)
+moe_layer_rows_staged_kernel(LayerArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t stage0[Staged<BF16, WK, true, 4>::kInstr * kWaves * 1024];
+    __shared__ __attribute__((aligned(1024))) uint8_t stage1[Staged<BF16, WK, true, 4>::kInstr * kWaves * 1024];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const LayerTable *const table = static_cast<const LayerTable *>(a.table);
+    const int expert = table->slot[blockIdx.y].expert, start = table->slot[blockIdx.y].start, n = table->slot[blockIdx.y].count;
+    if (expert < 0)
+        return;
+    const int h0 = (int(blockIdx.x) * kWaves + wave) * 2 * kCols;
+    by_rows<4>(n, [&](int r0, auto tiles) {
+        constexpr int NT = decltype(tiles)::value;
+        int none[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            none[t] = -1;
+        auto o = down_stream<BF16, WK, 2, NT, 2>(a, expert, h0, none, lane & 15);
+        Staged<BF16, WK, true, NT> s;
+        s.init([&](int r) { return r0 + r < n ? uint32_t(table->order[start + r0 + r]) * uint32_t(a.I) * 4 : o.x_end; }, wave, lane);
+        s.run(o, stage0, stage1, uint32_t(a.I) * 4, wave, lane);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int r = r0 + 16 * t + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int h = h0 + 16 * i + 4 * (lane >> 4);
+                if (r < n && h < a.H)
+                    *reinterpret_cast<f32x4 *>(a.rows + int64_t(table->order[start + r]) * a.H + h) = o.acc[t][i];
+            }
         }
     });
 }
@@ -553,9 +785,23 @@ hipError_t launch(const LayerArgs &a, hipStream_t stream)
         return parts;
     };
     auto groups = [](int slabs, int parts) { return uint32_t((slabs + kWaves / parts - 1) / (kWaves / parts)); };
+    // With several rows an expert, the tokens' values by way of LDS, as long as
+    // that makes workgroups for half of the chip (us for the whole layer, each
+    // kernel without and with it: 64 tokens, 4 of 4 experts of 4096 x 4096 bf16 247,
+    // first 172, both 131; 4 of 4 E4M3 139, 106, 91; 8 of 64 of 2048 x 1024 E4M3
+    // 119 and 95; 32 tokens, 8 of 64 of 1024 x 1024 bf16 94, 85, 81; 4 of 16 of
+    // 4096 x 2048 186, 189, 182; 8 tokens, 4 of 16 of 2048 x 2048 81, 88, 88 but 80.5
+    // with the second alone; too few workgroups: 30 tokens, 2 of 4 of 1024 x 1024
+    // 20, 23, 27)
+    auto staged = [&](int groups, int rows) { return choices >= rows * experts && int64_t(groups) * experts >= 128; };
     constexpr int TILES = tiles_of<WK>();
-    const int slabs = (a.I + 8 * TILES - 1) / (8 * TILES), parts = parts_for(slabs);
-    hipLaunchKernelGGL((moe_layer_up_kernel<BF16, WK>), dim3(groups(slabs, parts), experts), block, 0, stream, a, parts);
+    const int staged_up = (a.I + kWaves * kCols - 1) / (kWaves * kCols);
+    if (choices > kFewChoices && staged(staged_up, 4)) {
+        hipLaunchKernelGGL((moe_layer_up_staged_kernel<BF16, WK>), dim3(staged_up, experts), block, 0, stream, a);
+    } else {
+        const int slabs = (a.I + 8 * TILES - 1) / (8 * TILES), parts = parts_for(slabs);
+        hipLaunchKernelGGL((moe_layer_up_kernel<BF16, WK>), dim3(groups(slabs, parts), experts), block, 0, stream, a, parts);
+    }
     if (choices <= kFewChoices) {
         // waves that share an expert, as long as there is one for each
         int splits = 1;
@@ -563,11 +809,16 @@ hipError_t launch(const LayerArgs &a, hipStream_t stream)
             splits *= 2;
         hipLaunchKernelGGL((moe_layer_down_kernel<BF16, WK>), dim3((a.H + kCols - 1) / kCols), dim3(64 * kFewWaves), 0, stream,
                            a, experts, splits);
-    } else {
-        const int wide = (a.H + TILES * kCols - 1) / (TILES * kCols), shared = parts_for(wide);
-        hipLaunchKernelGGL((moe_layer_rows_kernel<BF16, WK>), dim3(groups(wide, shared), experts), block, 0, stream, a, shared);
-        hipLaunchKernelGGL(moe_layer_sum_kernel<BF16>, dim3((a.H + 1023) / 1024, a.T), dim3(256), 0, stream, a);
+        return hipGetLastError();
     }
+    const int staged_down = (a.H + 2 * kWaves * kCols - 1) / (2 * kWaves * kCols);
+    if (staged(staged_down, 2)) {
+        hipLaunchKernelGGL((moe_layer_rows_staged_kernel<BF16, WK>), dim3(staged_down, experts), block, 0, stream, a);
+    } else {
+        const int wide = (a.H + TILES * kCols - 1) / (TILES * kCols), parts = parts_for(wide);
+        hipLaunchKernelGGL((moe_layer_rows_kernel<BF16, WK>), dim3(groups(wide, parts), experts), block, 0, stream, a, parts);
+    }
+    hipLaunchKernelGGL(moe_layer_sum_kernel<BF16>, dim3((a.H + 1023) / 1024, a.T), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
