@@ -254,6 +254,11 @@ FP8 = [  # M, N, K, block, d
     (64, 2048, 2048, "tile", "bf16"), (64, 1027, 640, "row", "f16"), (65, 64, 384, "tile", "f32"), (100, 999, 1152, "row", "bf16"),
     (127, 128, 512, "tile", "bf16"), (129, 255, 272, "row", "f32"), (192, 640, 1024, "tile", "f16"), (257, 257, 528, "tile", "f32"),
     (333, 1003, 2064, "row", "f32"), (512, 768, 1536, "row", "bf16"), (700, 130, 96, "tile", "bf16"), (1030, 1300, 400, "tile", "f16"),
+    # wide weights: 32 columns a workgroup of the kernel for few rows, and tiles instead
+    (5, 8200, 272, "row", "bf16"), (20, 8200, 144, "tile", "f16"), (32, 8192, 128, "row", "f32"), (6, 8196, 2176, "tile", "f32"),
+    (17, 12300, 144, "row", "f16"), (2, 16400, 400, "tile", "bf16"),
+    # K split over workgroups
+    (40, 200, 6160, "row", "f32"), (130, 301, 6416, "tile", "f16"), (64, 2048, 8192, "tile", "bf16"), (500, 70, 7952, "row", "bf16"),
 ]
 
 
@@ -302,7 +307,88 @@ def test_fp8_exact(M, N, K, block, d):
     assert torch.equal(got.cpu(), ref.to(DT[d]))
 
 
-@pytest.mark.parametrize("M,N,K,d", [(3, 70, 144, "bf16"), (33, 131, 272, "f32"), (150, 203, 528, "f16"), (300, 260, 144, "bf16")])
+LARGE = [  # M, N, K, d: every tile that many workgroups choose, whole and ragged, 1 to 5 blocks
+    (4090, 4088, 272, "bf16"), (4091, 4095, 144, "f16"), (4096, 4096, 640, "f16"), (4097, 4104, 400, "bf16"),
+    (2000, 2000, 272, "bf16"), (2047, 2041, 144, "f16"), (1000, 2000, 528, "bf16"), (1023, 2050, 128, "f16"),
+    (4090, 4088, 272, "f32"), (2000, 2000, 400, "f32"), (1000, 2001, 144, "f32"),
+]
+
+
+@pytest.mark.parametrize("block", ["row", "tile"])
+@pytest.mark.parametrize("M,N,K,d", LARGE)
+def test_fp8_large_exact(M, N, K, d, block):
+    """As test_fp8_exact, every output of large products (the reference in 64 bits on the GPU), with and without an
+    old D of small whole numbers."""
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    kb = blocks(K)
+    A = torch.randint(-2, 3, (M, K), generator=g, device="cuda").float().to(E4M3)
+    B = torch.randint(-2, 3, (N, K), generator=g, device="cuda").float().to(E4M3)
+    SA = torch.exp2(torch.randint(0, 3, (kb, M), generator=g, device="cuda").float())
+    SB = torch.exp2(torch.randint(0, 3, (blocks(N), kb) if block == "tile" else (kb, N), generator=g, device="cuda").float())
+    a = A.double() * SA.t().double().repeat_interleave(128, 1)[:, :K]
+    s = SB.repeat_interleave(128, 0)[:N] if block == "tile" else SB.t()
+    ref = a @ (B.double() * s.double().repeat_interleave(128, 1)[:, :K]).t()
+    plan = mswz.gemm_fp8_plan_create(M, N, K, d, block)
+    ws = torch.empty(max(16, plan.workspace_bytes()), dtype=torch.uint8, device="cuda")
+    flat = torch.full((M * N + 64,), GUARD, dtype=DT[d], device="cuda")
+    D = flat[32:-32].view(M, N)
+    mswz.gemm_run_fp8(plan, A, SA, B, SB, D, workspace=ws)
+    assert torch.equal(D, ref.to(DT[d]))
+    D.copy_(torch.randint(-8, 9, (M, N), generator=g, device="cuda"))
+    old = D.double()
+    mswz.gemm_run_fp8(plan, A, SA, B, SB, D, beta=1, workspace=ws)
+    assert torch.equal(D, (ref + old).to(DT[d]))
+    D.fill_(GUARD)
+    assert (flat == GUARD).all()
+
+
+@pytest.mark.parametrize("block", ["row", "tile"])
+@pytest.mark.parametrize("M,N,K,d", [(4090, 4088, 912, "bf16"), (4097, 4099, 784, "f16"), (4090, 4088, 528, "f32"), (2000, 2000, 1040, "f16")])
+def test_fp8_large_sampled(M, N, K, d, block):
+    """Values of all sizes, whole rows and columns of large products."""
+    g = gen(M + K)
+    x = fp8_inputs(g, M, N, K, block)
+    plan = mswz.gemm_fp8_plan_create(M, N, K, d, block)
+    got = fp8_run(plan, x, torch.empty((M, N), dtype=DT[d], device="cuda")).cpu()
+    rows = torch.tensor([0, 1, 127, 128, 255, 256, 1000, M - 1])
+    ref, tol = fp8_reference(x["A"][rows], x["SA"][:, rows], x["B"], x["SB"], block == "tile", d == "f32")
+    close(got[rows], ref, tol, d, "rows")
+    cols = torch.tensor([0, 63, 64, 127, 128, 1000, N - 2, N - 1])
+    sb = x["SB"][cols // 128].t().contiguous() if block == "tile" else x["SB"][:, cols]
+    ref, tol = fp8_reference(x["A"], x["SA"], x["B"][cols], sb, False, d == "f32")
+    close(got[:, cols], ref, tol, d, "columns")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("block", ["row", "tile"])
+def test_quant_large(dt, block):
+    """A matrix whose outputs go past the caches equals its parts of 128 k rows."""
+    M, K, part = 8200, 4112, 1024
+    X = torch.randn(M, K, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(DT[dt])
+
+    def quantised(x):
+        m = x.shape[0]
+        plan = mswz.quant_fp8_plan_create(m, K, dt, block)
+        Q, QT = torch.empty(m, K, dtype=torch.uint8, device="cuda"), torch.empty(K, mp(m), dtype=torch.uint8, device="cuda")
+        S = torch.empty((blocks(K), m) if block == "row" else (blocks(m), blocks(K)), device="cuda")
+        ST = torch.empty((blocks(m), K) if block == "row" else (blocks(K), blocks(m)), device="cuda")
+        mswz.quant_fp8(plan, x, Q=Q, S=S, QT=QT, ST=ST)
+        return Q, S, QT, ST
+
+    Q, S, QT, ST = quantised(X)
+    for r in range(0, M, part):
+        x = X[r:r + part]
+        q, s, qt, st = quantised(x)
+        b, n = r // 128, x.shape[0]
+        assert torch.equal(Q[r:r + n], q) and torch.equal(QT[:, r:r + mp(n)], qt)
+        if block == "row":
+            assert torch.equal(S[:, r:r + n], s) and torch.equal(ST[b:b + blocks(n)], st)
+        else:
+            assert torch.equal(S[b:b + blocks(n)], s) and torch.equal(ST[:, b:b + blocks(n)], st)
+
+
+@pytest.mark.parametrize("M,N,K,d", [(3, 70, 144, "bf16"), (33, 131, 272, "f32"), (150, 203, 528, "f16"), (300, 260, 144, "bf16"),
+                                     (50, 131, 6288, "bf16"), (70, 90, 6160, "f32"), (2, 8200, 144, "f16"), (1000, 2000, 144, "bf16")])
 def test_fp8_pitches_and_surroundings(M, N, K, d):
     """Views with pitches, poison between their rows, D inside a guarded buffer at an odd element, a workspace with
     guards."""
@@ -350,9 +436,9 @@ def test_fp8_bad_rows_stay_apart():
             assert torch.equal(got[~bad.cuda()], clean[~bad.cuda()])
 
 
-def test_fp8_streams_graph_and_threads():
+@pytest.mark.parametrize("M,N,K", [(64, 1000, 2048), (64, 1000, 8192), (7, 1000, 2048)])
+def test_fp8_streams_and_graph(M, N, K):
     """Two streams with a workspace each, a captured call replayed between eager work, every result the same."""
-    M, N, K = 64, 1000, 2048
     x = fp8_inputs(gen(2), M, N, K, "tile")
     plan = mswz.gemm_fp8_plan_create(M, N, K, "bf16", "tile")
     want = fp8_run(plan, x, torch.empty((M, N), dtype=DT["bf16"], device="cuda")).clone()
@@ -388,6 +474,14 @@ def test_refusals_on_the_gpu():
             mswz.gemm_run_fp8(plan, *args)
     with pytest.raises(mswz.MswzError):
         mswz.gemm_run_fp8(plan, A, SA, B, SB, D, beta=2)
+    split = mswz.gemm_fp8_plan_create(64, 64, 8192, "f32", "row")
+    need = split.workspace_bytes()
+    assert need > 0
+    long = torch.zeros(64, 8192, dtype=torch.uint8, device="cuda")
+    s, D = torch.ones(64, 64, device="cuda"), torch.zeros(64, 64, device="cuda")
+    for ws in (None, torch.empty(need - 1, dtype=torch.uint8, device="cuda"), torch.empty(need, dtype=torch.uint8)):
+        with pytest.raises(ValueError):
+            mswz.gemm_run_fp8(split, long, s, long, s, D, workspace=ws)
     quant = mswz.quant_fp8_plan_create(4, 128)
     with pytest.raises(ValueError):
         mswz.quant_fp8(quant, D, Q=A, S=SA)

@@ -120,7 +120,42 @@ CASES = [  # T, k, E, H, I, dt, w, act
     (16, 4, 16, 1040, 144, "bf16", "e4m3", "silu"),
     (33, 3, 5, 144, 400, "f16", "e4m3", "silu"),
     (64, 8, 32, 256, 128, "bf16", "e4m3", "gelu"),
+    # many rows an expert: the tokens' values by way of LDS, in one kernel or both
+    (40, 8, 64, 264, 136, "bf16", "bf16", "silu"),
+    (60, 8, 64, 1032, 72, "f16", "f16", "gelu"),
+    (64, 8, 16, 1160, 520, "bf16", "bf16", "silu"),
+    (128, 8, 12, 1416, 712, "f16", "f16", "silu"),
+    (64, 8, 64, 272, 144, "bf16", "e4m3", "gelu"),
+    (96, 10, 40, 528, 208, "f16", "e4m3", "silu"),
+    (128, 8, 16, 1040, 528, "bf16", "e4m3", "silu"),
+    (100, 4, 2, 8208, 4104, "bf16", "bf16", "silu"),
 ]
+
+
+def skewed(x, T, k, E, seed):
+    """Choices of very unequal experts: one with half of them, some with one, some left out."""
+    g = torch.Generator().manual_seed(seed)
+    ids = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
+    ids[torch.rand(T, k, generator=g) < 0.5] = E // 2
+    ids[torch.rand(T, k, generator=g) < 0.05] = -1
+    ids[ids == E - 1] = E
+    x["ids"] = ids
+
+
+@pytest.mark.parametrize("T,k,E,H,I,dt,w", [
+    (64, 8, 64, 264, 136, "bf16", "bf16"), (64, 8, 64, 264, 136, "f16", "f16"), (64, 8, 64, 272, 144, "bf16", "e4m3"),
+    (64, 8, 64, 272, 144, "f16", "e4m3"), (70, 6, 5, 136, 72, "bf16", "bf16"), (70, 6, 5, 144, 80, "f16", "e4m3"),
+    (128, 8, 40, 520, 264, "bf16", "bf16"), (17, 1, 3, 72, 40, "f16", "f16"),
+])
+def test_unequal_experts(T, k, E, H, I, dt, w):
+    x = inputs(T * E, T, k, E, H, I, dt, w)
+    skewed(x, T, k, E, T)
+    plan = mswz.moe_layer_plan_create(T, k, E, H, I, dt, w)
+    ref, tol = reference(x, T, k, E, H, I, "silu")
+    got = run(plan, x, torch.full((T, H), float("nan"), dtype=DT[dt], device="cuda"))
+    close(got, ref, tol, dt)
+    again = run(plan, x, torch.zeros((T, H), dtype=DT[dt], device="cuda"))
+    assert torch.equal(got, again)
 
 
 @pytest.mark.parametrize("T,k,E,H,I,dt,w,act", CASES)
@@ -176,10 +211,12 @@ def test_wide_range():
     close(run(plan, x, torch.empty((T, H), dtype=DT["f16"], device="cuda")), ref, tol, "f16")
 
 
+@pytest.mark.parametrize("T,H", [(20, 144), (8, 144), (256, 5120)])
 @pytest.mark.parametrize("w", ["bf16", "e4m3"])
-def test_bad_values_stay_apart(w):
-    """A NaN token and an expert with infinite weights or scales reach the tokens that they belong to only."""
-    T, k, E, H, I = 20, 2, 5, 144, 144
+def test_bad_values_stay_apart(w, T, H):
+    """A NaN token and an expert with infinite weights or scales reach the tokens that they belong to only (a few
+    choices, more, and many for an expert with wide rows)."""
+    k, E, I = 2, 5, 144 if T < 100 else 2064
     x = inputs(13, T, k, E, H, I, "bf16", w)
     x["ids"] = torch.stack([torch.arange(T) % 4, torch.full((T,), -1)], 1).to(torch.int32).contiguous()
     plan = mswz.moe_layer_plan_create(T, k, E, H, I, "bf16", w)
@@ -200,9 +237,9 @@ def test_bad_values_stay_apart(w):
     assert not torch.isfinite(got[bad.cuda()][:, :128]).any()
 
 
-@pytest.mark.parametrize("T", [1, 18])
-def test_pitch_and_surroundings(T):
-    k, E, H, I, ld = 2, 4, 136, 72, 152
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 2, 4, 136, 72), (18, 2, 4, 136, 72), (64, 8, 64, 264, 136)])
+def test_pitch_and_surroundings(T, k, E, H, I):
+    ld = H + 16
     x = inputs(17, T, k, E, H, I, "bf16", "bf16")
     plan = mswz.moe_layer_plan_create(T, k, E, H, I, "bf16", ldx=ld)
     ref, tol = reference(x, T, k, E, H, I, "silu")
@@ -220,8 +257,8 @@ def test_pitch_and_surroundings(T):
     assert (ws[:32] == 0xA5).all() and (ws[32 + need:] == 0xA5).all()
 
 
-def test_streams_and_graph():
-    T, k, E, H, I = 6, 2, 8, 512, 256
+@pytest.mark.parametrize("T,k,E,H,I", [(6, 2, 8, 512, 256), (20, 2, 8, 512, 256), (64, 8, 64, 256, 136)])
+def test_streams_and_graph(T, k, E, H, I):
     x = inputs(19, T, k, E, H, I, "bf16", "bf16")
     other = inputs(20, T, k, E, H, I, "bf16", "bf16")
     plan = mswz.moe_layer_plan_create(T, k, E, H, I, "bf16")
