@@ -186,9 +186,12 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
     const bool beyond = int(16 * fp8_dma_chunk(wave, lane)) >= a.K % 128 && a.K % 128 != 0;
     auto issue = [&](uint8_t *stage, uint8_t *scales, int step) {
         const bool out = step >= step1 || (step == a.kb - 1 && beyond);
-        ca.issue(stage, step, out);
-        cb.issue(stage, step, out);
-        buffer_load_lds4(s_rsrc, scales + 256 * wave, step < step1 ? s_voff : s_bytes, s_step * uint32_t(step));
+        // (a step behind the last asks for nothing, from where the last one is:
+        // the scalar offset stays inside the buffers)
+        const int from = min(step, step1 - 1);
+        ca.issue(stage, from, out);
+        cb.issue(stage, from, out);
+        buffer_load_lds4(s_rsrc, scales + 256 * wave, step < step1 ? s_voff : s_bytes, s_step * uint32_t(from));
     };
 
     const int x16 = lane & 15, g = lane >> 4;

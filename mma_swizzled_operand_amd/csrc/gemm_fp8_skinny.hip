@@ -56,7 +56,9 @@ gemm_fp8_skinny_kernel(Fp8Args a, bool vec)
     const int n = u1 - u0, rot = n ? int(blockIdx.x / 8) % n : 0;
     auto load = [&](Block &d, int i) {
         const bool none = i >= n;
-        const int u = u0 + i + rot - (i + rot >= n ? n : 0);
+        // (behind the last from where the first is: the scalar offset stays inside
+        // the buffers)
+        const int u = none ? u0 : u0 + i + rot - (i + rot >= n ? n : 0);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const bool out = none || (u == a.kb - 1 && beyond[h]);

@@ -489,6 +489,47 @@ def test_refusals_on_the_gpu():
         mswz.quant_fp8(quant, torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda"), QT=A, ST=SA)
 
 
+def test_past_4_gib():
+    """Operands and results beyond 32 bits of offset: the last rows as those of a small call."""
+    K, N, M, part = 8192, 40, 540000, 300
+    gpu = torch.Generator(device="cuda").manual_seed(3)
+    X = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")      # 8.8 GB
+    X.normal_(generator=gpu)
+    plan = mswz.quant_fp8_plan_create(M, K, "bf16", "row")
+    Q, QT = torch.empty(M, K, dtype=E4M3, device="cuda"), torch.empty(K, mp(M), dtype=E4M3, device="cuda")   # 4.4 GB each
+    S, ST = torch.empty(blocks(K), M, device="cuda"), torch.empty(blocks(M), K, device="cuda")
+    mswz.quant_fp8(plan, X, Q=Q, S=S, QT=QT, ST=ST)
+    r0 = M // 128 * 128 - 256
+    tail = X[r0:]
+    q, s = torch.empty(M - r0, K, dtype=E4M3, device="cuda"), torch.empty(blocks(K), M - r0, device="cuda")
+    qt, st = torch.empty(K, mp(M - r0), dtype=E4M3, device="cuda"), torch.empty(blocks(M - r0), K, device="cuda")
+    mswz.quant_fp8(mswz.quant_fp8_plan_create(M - r0, K, "bf16", "row"), tail, Q=q, S=s, QT=qt, ST=st)
+    u8 = torch.uint8
+    assert torch.equal(Q[r0:].view(u8), q.view(u8)) and torch.equal(S[:, r0:], s)
+    assert torch.equal(QT.view(u8)[:, r0:], qt.view(u8)) and torch.equal(ST[r0 // 128:], st)
+    del X
+    B = (torch.randn(N, K, generator=gpu, device="cuda") * 100).clamp(-448, 448).to(E4M3)
+    SB = torch.rand(1, blocks(K), generator=gpu, device="cuda")
+    D = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    mswz.gemm_run_fp8(mswz.gemm_fp8_plan_create(M, N, K, "bf16", "tile"), Q, S, B, SB, D)
+    for rows in (slice(0, part), slice(M - part, M)):
+        a = Q[rows].double() * S[:, rows].t().double().repeat_interleave(128, 1)
+        b = B.double() * SB.double().repeat_interleave(128, 1)
+        ref = a @ b.t()
+        # the truncation is below 2^-10 of the terms' magnitudes (8 of 2^-13), D's rounding below 2^-8
+        assert ((D[rows].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -10 * (a.abs() @ b.abs().t())).all()
+    # the transposed values as B: N the larger side, with a pitch
+    wide = Q.view(u8).view(M // 2, 2 * K)[:, :K]
+    D = torch.zeros(16, M // 2, dtype=torch.bfloat16, device="cuda")
+    mswz.gemm_run_fp8(mswz.gemm_fp8_plan_create(16, M // 2, K, "bf16", "row", 0, 2 * K, 0), B[:16], SB.t().contiguous().expand(blocks(K), 16).contiguous(),
+                      wide, S[:, ::2].contiguous(), D)
+    cols = slice(M // 2 - part, M // 2)
+    a = B[:16].double() * SB.double().repeat_interleave(128, 1)
+    b = Q[::2][cols].double() * S[:, ::2][:, cols].t().double().repeat_interleave(128, 1)
+    ref = a @ b.t()
+    assert ((D[:, cols].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -10 * (a.abs() @ b.abs().t())).all()
+
+
 # ---- a linear layer trained with them -------------------------------------------------
 
 @pytest.mark.parametrize("M,N,K", [(100, 144, 272), (256, 128, 256), (1, 160, 128)])
