@@ -613,25 +613,33 @@ struct Staged {
                 for (int t = 0; t < NS; ++t)
                     d.s[t] = __builtin_bit_cast(float, buffer_load4(o.s_rsrc, u >= units ? o.s_end : o.s_row[t] + 4u * uint32_t(u / 2), 0));
     }
-    // o: rows and ranges; its sums are the result
-    __device__ void run(One &o, uint8_t *stage0, uint8_t *stage1, uint32_t token_bytes, int wave, int lane) const
+    // o: rows and ranges; its sums are the result.  The turn-th chunk is the first:
+    // workgroups and experts that start at different places keep all channels of
+    // the memory busy (us for the layer, all from the first chunk, neighbours'
+    // workgroups apart, and the experts too: 16 tokens, 4 of 32 experts of 4096 x
+    // 2048 bf16 228, 219, 216; 64, 4 of 4 of 4096 x 4096 131, 121, 119; 32, 4 of 16
+    // of 4096 x 2048 181, 189, 154; 64, 8 of 64 of 2048 x 1024 E4M3 96, 96, 96)
+    __device__ void run(One &o, uint8_t *stage0, uint8_t *stage1, uint32_t token_bytes, int turn, int wave, int lane) const
     {
         const int x16 = lane & 15, g = lane >> 4;
         const int units = int((o.row_bytes + 63) / 64), whole = WK == kWE4m3 ? (units + 1) & ~1 : units;
+        const int chunks = (whole + kUnits - 1) / kUnits, rot = turn % chunks;
+        auto place = [&](int c) { return c >= chunks ? chunks : c + rot - (c + rot >= chunks ? chunks : 0); };
 #pragma unroll
         for (int t = 0; t < NT; ++t)
             o.acc[t][0] = o.acc[t][1] = f32x4{};
         Unit d[kUnits];
-        copy(o, stage0, 0, token_bytes, wave);
+        copy(o, stage0, place(0), token_bytes, wave);
         static_for<0, kUnits>([&](auto i) {
-            load(o, d[i], i, whole, g, i % 2 == 1);
+            load(o, d[i], place(0) * kUnits + i, whole, g, i % 2 == 1);
             __builtin_amdgcn_sched_barrier(0);
         });
         lds_barrier_keep_vm<kLoads>();
         __builtin_amdgcn_sched_barrier(0);
         f32x4 part[NT][2];
         auto chunk = [&](const uint8_t *stage, uint8_t *next, int c) {
-            copy(o, next, c + 1, token_bytes, wave);
+            const int then = place(c + 1);
+            copy(o, next, then, token_bytes, wave);
             __builtin_amdgcn_sched_barrier(0);
             static_for<0, kUnits>([&](auto ic) {
                 constexpr int i = decltype(ic)::value;
@@ -661,13 +669,12 @@ struct Staged {
                                     o.acc[t][w][r] = fmaf(d[i].s[w % NS], part[t][w][r], o.acc[t][w][r]);
                     }
                 }
-                load(o, d[i], (c + 1) * kUnits + i, whole, g, i % 2 == 1);
+                load(o, d[i], then * kUnits + i, whole, g, i % 2 == 1);
                 __builtin_amdgcn_sched_barrier(0);
             });
             lds_barrier_keep_vm<kLoads>();
             __builtin_amdgcn_sched_barrier(0);
         };
-        const int chunks = (whole + kUnits - 1) / kUnits;
         for (int c = 0; c < chunks; c += 2) {
             chunk(stage0, stage1, c);
             if (c + 1 < chunks)
@@ -699,7 +706,7 @@ moe_layer_up_staged_kernel(LayerArgs a)
         Staged<BF16, WK, false, NT> s;
         s.init([&](int r) { return r0 + r < n ? uint32_t(rows[r0 + r] / uint32_t(a.topk)) * uint32_t(a.ldx) * 2 : o.x_end; },
                wave, lane);
-        s.run(o, stage0, stage1, uint32_t(a.H) * 2, wave, lane);
+        s.run(o, stage0, stage1, uint32_t(a.H) * 2, blockIdx.x / 4 + 3 * blockIdx.y, wave, lane);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int r = r0 + 16 * t + (lane & 15), i = i0 + 4 * (lane >> 4);
@@ -730,7 +737,7 @@ moe_layer_rows_staged_kernel(LayerArgs a)
         auto o = down_stream<BF16, WK, 2, NT, 2>(a, expert, h0, none, lane & 15);
         Staged<BF16, WK, true, NT> s;
         s.init([&](int r) { return r0 + r < n ? uint32_t(table->order[start + r0 + r]) * uint32_t(a.I) * 4 : o.x_end; }, wave, lane);
-        s.run(o, stage0, stage1, uint32_t(a.I) * 4, wave, lane);
+        s.run(o, stage0, stage1, uint32_t(a.I) * 4, blockIdx.x / 2 + 3 * blockIdx.y, wave, lane);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int r = r0 + 16 * t + (lane & 15);
