@@ -792,18 +792,19 @@ hipError_t launch(const LayerArgs &a, hipStream_t stream)
         return parts;
     };
     auto groups = [](int slabs, int parts) { return uint32_t((slabs + kWaves / parts - 1) / (kWaves / parts)); };
-    // With several rows an expert, the tokens' values by way of LDS, as long as
-    // that makes workgroups for half of the chip (us for the whole layer, each
-    // kernel without and with it: 64 tokens, 4 of 4 experts of 4096 x 4096 bf16 247,
-    // first 172, both 131; 4 of 4 E4M3 139, 106, 91; 8 of 64 of 2048 x 1024 E4M3
-    // 119 and 95; 32 tokens, 8 of 64 of 1024 x 1024 bf16 94, 85, 81; 4 of 16 of
-    // 4096 x 2048 186, 189, 182; 8 tokens, 4 of 16 of 2048 x 2048 81, 88, 88 but 80.5
-    // with the second alone; too few workgroups: 30 tokens, 2 of 4 of 1024 x 1024
-    // 20, 23, 27)
-    auto staged = [&](int groups, int rows) { return choices >= rows * experts && int64_t(groups) * experts >= 128; };
+    // With two rows an expert or more, the tokens' values by way of LDS, as long
+    // as that makes workgroups for half of the chip (us for the whole layer, with
+    // neither kernel, the first, the second, both: 64 tokens, 4 of 4 experts of
+    // 4096 x 4096 bf16 247, 161, 205, 119; E4M3 139, 99, 124, 85; 8 of 64 of 2048 x
+    // 1024 E4M3 119, 106, 110, 96; 32 tokens, 4 of 16 of 4096 x 2048 bf16 186, 171,
+    // 170, 154; 8 tokens, 4 of 16 of 2048 x 2048 bf16 81, -, 75.2, 75.0; E4M3 54.5,
+    // -, 52.7, 47.6; the other way 10 tokens, 5 of 10 of 2048 x 2048 -, 74, 65, 72,
+    // whose 320 and 160 workgroups fill the chip badly; too few workgroups: 30
+    // tokens, 2 of 4 of 1024 x 1024 20, 23, -, 27)
+    auto staged = [&](int groups) { return choices >= 2 * experts && int64_t(groups) * experts >= 128; };
     constexpr int TILES = tiles_of<WK>();
     const int staged_up = (a.I + kWaves * kCols - 1) / (kWaves * kCols);
-    if (choices > kFewChoices && staged(staged_up, 4)) {
+    if (choices > kFewChoices && staged(staged_up)) {
         hipLaunchKernelGGL((moe_layer_up_staged_kernel<BF16, WK>), dim3(staged_up, experts), block, 0, stream, a);
     } else {
         const int slabs = (a.I + 8 * TILES - 1) / (8 * TILES), parts = parts_for(slabs);
@@ -819,7 +820,7 @@ hipError_t launch(const LayerArgs &a, hipStream_t stream)
         return hipGetLastError();
     }
     const int staged_down = (a.H + 2 * kWaves * kCols - 1) / (2 * kWaves * kCols);
-    if (staged(staged_down, 2)) {
+    if (staged(staged_down)) {
         hipLaunchKernelGGL((moe_layer_rows_staged_kernel<BF16, WK>), dim3(staged_down, experts), block, 0, stream, a);
     } else {
         const int wide = (a.H + TILES * kCols - 1) / (TILES * kCols), parts = parts_for(wide);
