@@ -62,13 +62,13 @@ void moe_layer_plan_destroy(moe_layer_plan *plan);
 int64_t moe_layer_plan_workspace_size(const moe_layer_plan *plan);
 
 /*
- * Enqueue the layer (two kernels).  ids int32 [T][topk], a choice outside
- * 0 .. E-1 is left out (a token without any gives zeros); an expert may be
- * chosen twice; w fp32 [T][topk].  S1 and S2 are given exactly for E4M3
- * weights.  X, W1, W2, Y and workspace are 16-byte aligned, the others 4-byte.
- * The workspace is the caller's, its contents before the call do not matter,
- * and calls that may overlap must not share it, replays of two captured graphs
- * among them.
+ * Enqueue the layer: two kernels for up to 16 choices, three for more.  ids
+ * int32 [T][topk], a choice outside 0 .. E-1 is left out (a token without any
+ * gives zeros); an expert may be chosen twice; w fp32 [T][topk].  S1 and S2 are
+ * given exactly for E4M3 weights.  X, W1, W2, Y and workspace are 16-byte
+ * aligned, the others 4-byte.  The workspace is the caller's, its contents
+ * before the call do not matter, and calls that may overlap must not share it,
+ * replays of two captured graphs among them.
  * Returns MSWZ_OK, MSWZ_ERR_INVALID, MSWZ_ERR_ALIGN or MSWZ_ERR_HIP.
  */
 int moe_layer(const moe_layer_plan *plan, const void *X, const int32_t *ids, const float *w,

@@ -1,7 +1,7 @@
 // experts_abi.hip — the C ABI declared in include/mswz_experts.h and
-// include/mswz_moe_layer.h: plan creation, argument checks and dispatch of the expert operators, in abi.hip's
-// manner: everything the library cannot run is rejected with a status before
-// any GPU work.
+// include/mswz_moe_layer.h: plan creation, argument checks and dispatch of the
+// expert operators, in abi.hip's manner: everything the library cannot run is
+// rejected with a status before any GPU work.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

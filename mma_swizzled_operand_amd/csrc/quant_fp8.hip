@@ -10,6 +10,9 @@
 // 256-byte row pieces over 16 lanes, a block along a row is reduced over those
 // 16 lanes, and the 8 rows of a column are 8 consecutive bytes of QT, which go
 // through LDS into whole 128-byte lines.
+//
+// Bound by the memory: 16384 x 4096 bf16 by rows, both ways, 58.4 us; 8192 x 8192
+// by tiles, both ways, 57.2; 4.7 TB/s (a copy: 4.9).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

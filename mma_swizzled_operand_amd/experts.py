@@ -1,7 +1,8 @@
-"""Binding of the expert operators (include/mswz_experts.h, mswz_moe_layer.h): products with
-4-bit weights, products over rows grouped by expert, the token movement around
-them, and a whole layer of experts for a few tokens.  Names and arguments are the C ABI's.  Tensors are checked against
-the plan's sizes and types and must share one GPU; a call runs on that GPU, on
+"""Binding of the expert operators (include/mswz_experts.h and
+mswz_moe_layer.h): products with 4-bit weights, products over rows grouped by
+expert, the token movement around them, and a whole layer of experts for a few
+tokens.  Names and arguments are the C ABI's.  Tensors are checked against the
+plan's sizes and types and must share one GPU; a call runs on that GPU, on
 ``stream`` (default: torch's current stream of that GPU).
 
     moe = moe_plan_create(T, topk, E, H, "bf16")
