@@ -14,11 +14,21 @@ namespace {
 int64_t tiles(const Fp8Args &a, int bm, int bn) { return int64_t((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); }
 
 // Whether a few rows of A take the kernel without barriers
-// (gemm_fp8_skinny.hip): up to 32, unless there are enough tiles of 64 x 64 for
-// the chip, which fetch whole lines (K 4096 by 4096 columns, one row: 7.8 us,
-// tiles 12.4; 16: 8.0 and 12.4; 32: 9.9 and 12.6.  K 8192 by 16384, 16: 32.0 and
-// 31.4; 32: 36.4 and 32.5; 64: 45 and 35).
-bool is_skinny(const Fp8Args &a) { return a.M <= 32 && tiles(a, 64, 64) < (a.M > 16 ? 192 : 256); }
+// (gemm_fp8_skinny.hip): up to 32, as long as there are few columns; with more, the
+// tiles fetch whole lines.  us, without barriers and by tiles, 16-bit D: 2 rows of
+// 4096 by 4096 columns 7.4 and 10.1, of 8192 by 4096 9.5 and 12.0, of 4096 by 6144
+// 11.5 and 11.6, of 8192 by 12288 23.6 and 22.8; 16 rows 8.0 and 10.2, 11.7 and
+// 12.3, 12.8 and 11.9, 34.7 and 23.9; 32 rows 9.4 and 10.3, 16.7 and 13.1 (tiles
+// with K split), 18.6 and 12.5, 43 and 26.  K 2048: within 10 %.  An fp32 D's tiles
+// have two to four times the work at a step: 8 rows of 8192 by 8192 18.2 and 21.5,
+// by 16384 36 and 26; 16 rows of 4096 by 8192 12.9 and 13.8, of 8192 by 5120 20.3
+// and 18.3.
+bool is_skinny(const Fp8Args &a)
+{
+    if (a.M <= 16)
+        return tiles(a, 64, 64) <= (a.out == kOutF32 ? 128 : 64);
+    return a.M <= 32 && tiles(a, 64, 64) <= 64 && a.kb < 48;
+}
 
 // K parts of a product: where tiles of 64 x 64 leave half of the compute units
 // idle and K is long, it is split until there are as many, each part keeping
