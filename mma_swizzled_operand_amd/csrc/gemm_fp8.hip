@@ -61,12 +61,12 @@ fp8_reduce_kernel(Fp8Args a, int parts, bool vec)
     fp8_store(a, m, n, v, vec);
 }
 
-template <int BM, int BN, int WM, int WN, int S, bool ROWB, int OUT>
+template <int BM, int BN, int WM, int WN, int S, int P, bool ROWB, int OUT>
 hipError_t launch_tile(const Fp8Args &a, hipStream_t stream, int parts = 1)
 {
     const int tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN, per = (a.kb + parts - 1) / parts;
     parts = (a.kb + per - 1) / per;
-    hipLaunchKernelGGL((gemm_fp8_kernel<BM, BN, WM, WN, S, ROWB, OUT == kOutF32, OUT>),
+    hipLaunchKernelGGL((gemm_fp8_kernel<BM, BN, WM, WN, S, P, ROWB, OUT == kOutF32, OUT>),
                        dim3(uint32_t(tiles_m) * uint32_t(tiles_n), parts), dim3(64 * (BM / WM) * (BN / WN)), 0, stream, a,
                        tiles_m, tiles_n, -4, per, parts == 1 && fp8_whole_lines(a) ? 2 : int(fp8_whole_stores(a)));
     if (parts > 1)
@@ -80,7 +80,7 @@ hipError_t launch_out(const Fp8Args &a, hipStream_t stream)
 {
     const int parts = parts_of(a);
     if (parts > 1)
-        return launch_tile<64, 64, 32, 32, 4, ROWB, OUT>(a, stream, parts);
+        return launch_tile<64, 64, 32, 32, 6, 2, ROWB, OUT>(a, stream, parts);
     // The tile whose rounds over the chip take the least time.  A tile's time,
     // in units of 10 ns for one block of K, is what one round took (K 4096, 16-bit
     // D); the compute units hold one workgroup each but for the tile of 128 x 128
@@ -103,14 +103,14 @@ hipError_t launch_out(const Fp8Args &a, hipStream_t stream)
         if (all[i].rounds * all[i].time <= all[best].rounds * all[best].time)
             best = i;
     switch (best) {
-    case 0: return launch_tile<32, 64, 16, 32, 4, ROWB, OUT>(a, stream);
-    case 1: return launch_tile<64, 64, 32, 32, 4, ROWB, OUT>(a, stream);
-    case 2: return launch_tile<128, 64, 32, 32, 4, ROWB, OUT>(a, stream);
-    case 3: return launch_tile<128, 128, 64, 32, 4, ROWB, OUT>(a, stream);
-    case 4: return launch_tile<128, 128, 64, 64, 2, ROWB, OUT>(a, stream);
+    case 0: return launch_tile<32, 64, 16, 32, 6, 2, ROWB, OUT>(a, stream);
+    case 1: return launch_tile<64, 64, 32, 32, 4, 1, ROWB, OUT>(a, stream);
+    case 2: return launch_tile<128, 64, 32, 32, 4, 1, ROWB, OUT>(a, stream);
+    case 3: return launch_tile<128, 128, 64, 32, 4, 1, ROWB, OUT>(a, stream);
+    case 4: return launch_tile<128, 128, 64, 64, 2, 1, ROWB, OUT>(a, stream);
     }
     if constexpr (OUT != kOutF32)
-        return launch_tile<256, 256, 128, 64, 2, ROWB, OUT>(a, stream);
+        return launch_tile<256, 256, 128, 64, 2, 1, ROWB, OUT>(a, stream);
     return hipErrorUnknown;
 }
 

@@ -141,9 +141,10 @@ struct Fp8Copy {
     }
 };
 
-// BM x BN outputs a workgroup, WM x WN a wave, S stages in LDS.  ROWB: B's scales belong to
+// BM x BN outputs a workgroup, WM x WN a wave, S stages in LDS, P blocks from one
+// barrier to the next.  ROWB: B's scales belong to
 // rows (else to 128 x 128 tiles).  EXACT: by way of bf16.  OUT: D's kind.
-template <int BM, int BN, int WM, int WN, int S, bool ROWB, bool EXACT, int OUT>
+template <int BM, int BN, int WM, int WN, int S, int P, bool ROWB, bool EXACT, int OUT>
 __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN))
 gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_part, int vec)
 {
@@ -157,13 +158,17 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
     __shared__ __attribute__((aligned(1024))) uint8_t lds1[kAB];
     __shared__ __attribute__((aligned(1024))) uint8_t lds2[S > 2 ? kAB : 16];
     __shared__ __attribute__((aligned(1024))) uint8_t lds3[S > 3 ? kAB : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds4[S > 4 ? kAB : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds5[S > 5 ? kAB : 16];
     __shared__ __attribute__((aligned(256))) uint8_t scl0[256 * W];
     __shared__ __attribute__((aligned(256))) uint8_t scl1[256 * W];
     __shared__ __attribute__((aligned(256))) uint8_t scl2[S > 2 ? 256 * W : 16];
     __shared__ __attribute__((aligned(256))) uint8_t scl3[S > 3 ? 256 * W : 16];
+    __shared__ __attribute__((aligned(256))) uint8_t scl4[S > 4 ? 256 * W : 16];
+    __shared__ __attribute__((aligned(256))) uint8_t scl5[S > 5 ? 256 * W : 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    auto stage = [&](auto n) { return std::get<decltype(n)::value>(std::make_tuple(lds0, lds1, lds2, lds3)); };
-    auto scales_of = [&](auto n) { return std::get<decltype(n)::value>(std::make_tuple(scl0, scl1, scl2, scl3)); };
+    auto stage = [&](auto n) { return std::get<decltype(n)::value>(std::make_tuple(lds0, lds1, lds2, lds3, lds4, lds5)); };
+    auto scales_of = [&](auto n) { return std::get<decltype(n)::value>(std::make_tuple(scl0, scl1, scl2, scl3, scl4, scl5)); };
     int tm, tn;
     tile_of_block(blockIdx.x, tiles_m, tiles_n, group_m, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
@@ -274,27 +279,38 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
                 for (int r = 0; r < 4; ++r)
                     acc[j][i][r] = fmaf(v[r], ROWB ? sav[i] * sbv[ROWB ? j : 0][r] : sav[i], acc[j][i][r]);
             }
-            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (P == 1)
+                __builtin_amdgcn_sched_barrier(0);
         });
     };
-    // a step ends when the next one's copies are in LDS; those of the S - 2
-    // steps after it stay in flight (six stages of 64 x 64: 64 x 16384 x 8192 33.4
-    // us, 32.2 with four)
+    // P steps end when the next ones' copies are in LDS; those of the steps after
+    // them stay in flight.  (Six stages of 64 x 64 in place of four: 64 x 16384 x 8192
+    // 33.4 and 32.2 us.  Two steps a barrier where latency counts, of six stages: 333 x
+    // 1003 x 2064 fp32 11.2 -> 10.4 us, bf16 8.8 -> 8.3, 100 x 1000 x 4096 9.9 -> 8.9;
+    // of four, whose copies have less time: 10.5, 10.1, 12.0.  Where the memory counts,
+    // 64 x 16384 x 8192, 32.5 -> 32.9.)
     constexpr int kCopies = decltype(ca)::kInstr + decltype(cb)::kInstr + 1;
     auto step_end = [] {
         __builtin_amdgcn_sched_barrier(0);
-        lds_barrier_keep_vm<(S - 2) * kCopies>();
+        lds_barrier_keep_vm<(S - 2 * P) * kCopies>();
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    static_for<0, S - 1>([&](auto n) { issue(stage(n), scales_of(n), step0 + n); });
+    static_for<0, S - P>([&](auto n) { issue(stage(n), scales_of(n), step0 + n); });
     step_end();
     // (steps behind the last are of zeros)
     for (int k = step0; k < step1; k += S)
-        static_for<0, S>([&](auto n) {
-            constexpr int next = (n + S - 1) % S;
-            issue(stage(std::integral_constant<int, next>{}), scales_of(std::integral_constant<int, next>{}), k + n + S - 1);
-            compute(stage(n), scales_of(n));
+        static_for<0, S / P>([&](auto n) {
+            if (P > 1 && n > 0 && k + P * n >= step1)   // (few tiles, short K: none of zeros alone)
+                return;
+            static_for<0, P>([&](auto i) {
+                constexpr int next = (P * n + S - P + i) % S;
+                issue(stage(std::integral_constant<int, next>{}), scales_of(std::integral_constant<int, next>{}), k + P * n + S - P + i);
+            });
+            static_for<0, P>([&](auto i) {
+                constexpr int now = P * n + i;
+                compute(stage(std::integral_constant<int, now>{}), scales_of(std::integral_constant<int, now>{}));
+            });
             step_end();
         });
     lds_barrier_keep_vm<0>();   // no copy may still be writing LDS when the workgroup ends
