@@ -22,7 +22,7 @@
 // PFLOP/s; MFMAs busy 61 %, the rest of a step is copies into LDS, fragment
 // reads and the barrier.  Both gradients of 8192 x 4096 x 4096 257 us, 2.14
 // PFLOP/s (MFMAs busy 51 % with tile scales; 45 % with row scales, which take a
-// second multiplication a value).  64 x 16384 x 8192 32.2 us, 4.3 TB/s: as many
+// second multiplication a value).  64 x 16384 x 8192 31.8 us, 4.3 TB/s: as many
 // bytes again come from the L2, A for every workgroup.
 #pragma once
 #include <hip/hip_runtime.h>
