@@ -342,6 +342,22 @@ def test_fp8_large_exact(M, N, K, d, block):
     assert (flat == GUARD).all()
 
 
+STEPS = [(40, 700, k, d) for k, d in ((16, "bf16"), (128, "f32"), (144, "f16"), (272, "bf16"), (640, "f16"), (816, "f32"),
+                                      (896, "bf16"), (1648, "f32"))]
+STEPS += [(17, 8200, 1040, "bf16"), (5, 12000, 400, "f16"), (5, 16400, 656, "f32"), (64, 16000, 656, "bf16"),
+          (500, 4000, 912, "f16"), (1000, 3900, 784, "bf16"), (2000, 3900, 528, "bf16"), (2000, 3900, 400, "f32"),
+          (4000, 3900, 400, "f16"), (60, 2000, 6416, "bf16"), (60, 2000, 6416, "f32"), (16, 4000, 1040, "bf16"),
+          (32, 4090, 784, "f16"), (9, 8100, 656, "f32")]
+
+
+@pytest.mark.parametrize("block", ["row", "tile"])
+@pytest.mark.parametrize("M,N,K,d", STEPS)
+def test_fp8_steps_exact(M, N, K, d, block):
+    """As test_fp8_large_exact: K of one to thirteen blocks by the smallest tile, then every tile, with workgroups that
+    start inside K and a last block that ends inside it."""
+    test_fp8_large_exact(M, N, K, d, block)
+
+
 @pytest.mark.parametrize("block", ["row", "tile"])
 @pytest.mark.parametrize("M,N,K,d", [(4090, 4088, 912, "bf16"), (4097, 4099, 784, "f16"), (4090, 4088, 528, "f32"), (2000, 2000, 1040, "f16")])
 def test_fp8_large_sampled(M, N, K, d, block):

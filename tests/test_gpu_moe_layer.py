@@ -170,6 +170,14 @@ def test_layer(T, k, E, H, I, dt, w, act):
     assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("T,k,E,H,I,w", [(64, 8, 48, 1032, 520, "bf16"), (64, 8, 48, 1040, 528, "e4m3"), (20, 4, 36, 1096, 600, "bf16"),
+                                         (20, 4, 36, 1104, 592, "e4m3")])
+def test_layer_starts_inside_rows(T, k, E, H, I, w):
+    """Two choices an expert and more, many experts: workgroups that start at every place of a row whose last chunk is
+    not whole."""
+    test_layer(T, k, E, H, I, "bf16", w, "gelu")
+
+
 @pytest.mark.parametrize("w", ["bf16", "e4m3"])
 def test_choices_left_out(w):
     """Ids of other devices, tokens without any expert, all tokens to one expert, the same expert twice."""
