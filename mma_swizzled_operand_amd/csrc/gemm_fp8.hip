@@ -81,41 +81,51 @@ hipError_t launch_out(const Fp8Args &a, hipStream_t stream)
     const int parts = parts_of(a);
     if (parts > 1)
         return launch_tile<64, 64, 32, 32, 6, 2, ROWB, OUT>(a, stream, parts);
-    // The tile whose rounds over the chip take the least time.  A tile's time,
-    // in units of 10 ns for one block of K, is what one round took (K 4096, 16-bit
-    // D); the compute units hold one workgroup each but for the second form of 128
-    // x 128, of which they hold two.  (us in the order of the table, tile scales,
-    // bf16 D: 64 x 4096 x 4096 9.7, 12.6, 14.3, 18.3, 24.8, 44.2; 256 x 4096 x 4096 17.1,
-    // 13.0, 15.4, 19.0, 25.7, 46.7; 512 x 4096 x 4096 28.7, 21.3, 17.7, 22.3, 31.3,
-    // 49.5; 1024 x 4096 x 4096 51.0, 36.6, 32.8, 23.3, 31.6, 50.0; 2048 x 4096 x 4096 95,
-    // 66, 60, 43.6, 39.2, 51.3; 4096 x 4096 x 4096 186, 129, 116, 85, 76, 61.)  The
-    // largest does not leave the bf16 form registers, so an fp32 D stops at 128 x
-    // 128 (4096 x 4096 x 4096 128 us, 238 with it).
+    // The tile whose rounds over the chip take the least time.  A round takes
+    // `start` and `step` for each block of K, `uneven` more where rows are not whole
+    // lines of 128 bytes (a copied row then costs two), in units of 10 ns, fitted to
+    // the times below; the compute units hold one workgroup each but for the second
+    // form of 128 x 128, of which they hold two.  us in the order of the table, tile
+    // scales, bf16 D: 64 x 4096 x 4096 9.7, 12.6, 14.3, 18.3, 24.8, 44.2; 256 x 4096 x
+    // 4096 17.1, 13.0, 15.4, 19.0, 25.7, 46.7; 512 x 4096 x 4096 28.7, 21.3, 17.7, 22.3,
+    // 31.3, 49.5; 1024 x 4096 x 4096 51.0, 36.6, 32.8, 23.3, 31.6, 50.0; 2048 x 4096 x
+    // 4096 95, 66, 60, 43.6, 39.2, 51.3; 2048 x 4096 x 1024 35.2, 21.0, 20.7, 14.9,
+    // 11.7, 17.3; 4096 x 4096 x 4096 186, 129, 116, 85, 76, 61; 5432 x 3696 x 1712 -, 86,
+    // 86, 73, 61, 60.  The largest does not leave the bf16 form registers, so an fp32
+    // D stops at 128 x 128 (4096 x 4096 x 4096 128 us, 238 with it).
     // Waves of 64 columns store whole lines (waves of 32 rows by 64 columns and of 64
     // by 32 in the first form of 128 x 128: 1024 x 4096 x 4096 23.3 and 26.5 us).  In
     // the second form eight waves of 32 x 64 hide more than four of 64 x 64, if both
     // workgroups' registers fit (2048 x 4096 x 4096 39.1 and 41.0 us; row scales 63.6
     // and 50.0, fp32 D 79.8 and 71.6).
+    constexpr bool F32 = OUT == kOutF32;
     const struct {
-        int64_t rounds, time;
-    } all[6] = {{(tiles(a, 32, 64) + 255) / 256, 17},
-                {(tiles(a, 64, 64) + 255) / 256, 25},
-                {(tiles(a, 128, 64) + 255) / 256, 42},
-                {(tiles(a, 128, 128) + 255) / 256, 72},
-                {(tiles(a, 128, 128) + 511) / 512, 135},
-                {(tiles(a, 256, 256) + 255) / 256, 200}};
+        int64_t tiles, slots, step, uneven, start;
+    } all[6] = {{tiles(a, 32, 64), 256, F32 ? 24 : 16, 4, 40},
+                {tiles(a, 64, 64), 256, F32 ? 39 : 25, 6, 30},
+                {tiles(a, 128, 64), 256, F32 ? 77 : 41, 10, 140},
+                {tiles(a, 128, 128), 256, F32 ? 119 : 64, 16, 130},
+                {tiles(a, 128, 128), 512, F32 ? 205 : 115, 17, 150},
+                {tiles(a, 256, 256), 256, 165, 12, 400}};
+    const bool uneven = a.lda % 128 != 0 || a.ldb % 128 != 0;
     int best = 0;
-    for (int i = 1; i < (OUT == kOutF32 ? 5 : 6); ++i)
-        if (all[i].rounds * all[i].time <= all[best].rounds * all[best].time)
+    int64_t least = INT64_MAX;
+    for (int i = 0; i < (F32 ? 5 : 6); ++i) {
+        const int64_t time = (all[i].tiles + all[i].slots - 1) / all[i].slots *
+                             ((all[i].step + (uneven ? all[i].uneven : 0)) * a.kb + all[i].start);
+        if (time <= least) {
+            least = time;
             best = i;
+        }
+    }
     switch (best) {
     case 0: return launch_tile<32, 64, 16, 32, 6, 2, ROWB, OUT>(a, stream);
     case 1: return launch_tile<64, 64, 16, 64, 4, 1, ROWB, OUT>(a, stream);
     case 2: return launch_tile<128, 64, 16, 64, 4, 1, ROWB, OUT>(a, stream);
     case 3: return launch_tile<128, 128, 32, 64, 4, 1, ROWB, OUT>(a, stream);
-    case 4: return launch_tile<128, 128, ROWB || OUT == kOutF32 ? 64 : 32, 64, 2, 1, ROWB, OUT>(a, stream);
+    case 4: return launch_tile<128, 128, ROWB || F32 ? 64 : 32, 64, 2, 1, ROWB, OUT>(a, stream);
     }
-    if constexpr (OUT != kOutF32)
+    if constexpr (!F32)
         return launch_tile<256, 256, 128, 64, 2, 1, ROWB, OUT>(a, stream);
     return hipErrorUnknown;
 }
