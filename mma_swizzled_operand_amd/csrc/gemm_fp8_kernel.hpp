@@ -141,6 +141,16 @@ struct Fp8Copy {
     }
 };
 
+// PAST: past the caches.
+template <bool PAST, typename V>
+__device__ __forceinline__ void store(V *to, V v)
+{
+    if constexpr (PAST)
+        __builtin_nontemporal_store(v, to);
+    else
+        *to = v;
+}
+
 // BM x BN outputs a workgroup, WM x WN a wave, S stages in LDS, P blocks from one
 // barrier to the next.  ROWB: B's scales belong to
 // rows (else to 128 x 128 tiles).  EXACT: by way of bf16.  OUT: D's kind.
@@ -315,15 +325,16 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
         });
     lds_barrier_keep_vm<0>();   // no copy may still be writing LDS when the workgroup ends
 
-    // 16-bit D, 64 columns a wave: the tile goes through LDS (16-byte chunk c of
-    // row r at place c ^ (r % 8) of its 128 bytes) and out as whole lines past the
-    // caches, as long as every piece of 16 bytes is aligned
+    // 16-bit D without an old one, 64 columns a wave: the tile goes through LDS
+    // (16-byte chunk c of row r at place c ^ (r % 8) of its 128 bytes) and out row by
+    // row: as whole lines past the caches where every piece of 16 bytes is
+    // aligned, else in pieces of four values or one (a lane's four columns at once:
+    // 5432 x 3691 x 1712 104 us, 79 this way; 8192 x 8191 x 8192 514 and 461)
     if constexpr (OUT != kOutF32 && WN == 64) {
         static_assert(BM * BN * 2 <= 2 * kAB && (BM * BN * 2 <= kAB || W % 2 == 0), "in two stages");
-        if (vec == 2) {
+        if (!a.beta && gridDim.y == 1) {
             using T = std::conditional_t<OUT == kOutBf16, __bf16, _Float16>;
             typedef T t4 __attribute__((ext_vector_type(4)));
-            typedef T t8 __attribute__((ext_vector_type(8)));
             constexpr int kMine = WM * 128, kFit = kAB / kMine;   // waves whose tiles one stage holds
             uint8_t *const mine = (wave < kFit ? lds0 : lds1) + wave % kFit * kMine;
 #pragma unroll
@@ -335,15 +346,28 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
                         t4{T(acc[j][i][0]), T(acc[j][i][1]), T(acc[j][i][2]), T(acc[j][i][3])};
                 }
             wave_lds_sync();
-            const int n = n0 + wn + 8 * (lane & 7);
+            T *const d = static_cast<T *>(a.D);
+            // WIDE values a lane, 64 / WIDE lanes a row
+            auto rows = [&](auto wide, auto past) {
+                constexpr int WIDE = decltype(wide)::value, LANES = 64 / WIDE;
+                typedef T piece __attribute__((ext_vector_type(WIDE)));
+                const int c = lane % LANES, n = n0 + wn + WIDE * c;
 #pragma unroll 4
-            for (int k = 0; k < WM / 8; ++k) {
-                const uint32_t r = 8 * k + (lane >> 3);
-                const int m = m0 + wm + int(r);
-                if (m < a.M && n < a.N)
-                    __builtin_nontemporal_store(*reinterpret_cast<const t8 *>(mine + r * 128 + (((lane & 7) ^ (r & 7)) << 4)),
-                                                reinterpret_cast<t8 *>(static_cast<T *>(a.D) + int64_t(m) * a.ldd + n));
-            }
+                for (int k = 0; k < WM * LANES / 64; ++k) {
+                    const uint32_t r = 64 / LANES * k + lane / LANES;
+                    const int m = m0 + wm + int(r);
+                    if (m < a.M && n < a.N)
+                        store<decltype(past)::value>(reinterpret_cast<piece *>(d + int64_t(m) * a.ldd + n),
+                                                     *reinterpret_cast<const piece *>(mine + r * 128 + (((WIDE * c / 8) ^ (r & 7)) << 4) +
+                                                                                      2 * (WIDE * c % 8)));
+                }
+            };
+            if (vec == 2)
+                rows(std::integral_constant<int, 8>{}, std::true_type{});
+            else if (vec == 1)
+                rows(std::integral_constant<int, 4>{}, std::false_type{});
+            else
+                rows(std::integral_constant<int, 1>{}, std::false_type{});
             return;
         }
     }
