@@ -14,9 +14,9 @@
 // choices an expert or more, both products take the tokens' values from LDS
 // (Staged).
 //
-// 16 tokens, 4 of 32 experts of 4096 x 2048 bf16: 215 us, kernels 143, 71 and 3, 5.8
+// 16 tokens, 4 of 32 experts of 4096 x 2048 bf16: 215 us, kernels 143, 70 and 5, 5.8
 // TB/s of weights (a copy: 4.9).  64 tokens, 8 of 64 of 2048 x 1024 E4M3: 94 us,
-// kernels 56, 33 and 3, 4.5 TB/s while they run: their starts and ends are a
+// kernels 56, 33 and 5, 4.5 TB/s while they run: their starts and ends are a
 // larger share.  One token, 2 of 8 of 1024 x 512: 12 us, two launches of three
 // dependent reads each.
 //
@@ -761,10 +761,11 @@ moe_layer_rows_staged_kernel(LayerArgs a)
 }
 
 // y[t] = sum_j w[t][j] rows[t][j], in the order of j; four columns a thread,
-// the reads of eight choices at once (those of a choice left out, whatever lies
-// there, and of the last one again, are not used): one after the other the layer
-// of 64 tokens, 8 of 64 experts of 2048 x 1024 E4M3 took 96.1 us, this way 94.2, that
-// of 8 tokens, 8 of 64 of 512 x 256 19.3 and 17.9.
+// the ids and weights of eight choices read at once (whatever lies where a choice
+// is left out is not used): one choice after the other the layer of 64 tokens, 8
+// of 64 experts of 2048 x 1024 E4M3 took 96.1 us, this way 94.2, that of 8 tokens,
+// 8 of 64 of 512 x 256 19.3 and 17.9; the rows' reads pinned before the first sum:
+// no more.
 template <bool BF16>
 __global__ void __launch_bounds__(kSumThreads)
 moe_layer_sum_kernel(LayerArgs a)
