@@ -327,8 +327,8 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
 
     // 16-bit D without an old one, 64 columns a wave: the tile goes through LDS
     // (16-byte chunk c of row r at place c ^ (r % 8) of its 128 bytes) and out row by
-    // row: as whole lines past the caches where every piece of 16 bytes is
-    // aligned, else in pieces of four values or one (a lane's four columns at once:
+    // row: as whole lines past the caches where N is whole pieces of 16 bytes and
+    // every one is aligned, else in pieces of four values or one (a lane's four columns at once:
     // 5432 x 3691 x 1712 104 us, 79 this way; 8192 x 8191 x 8192 514 and 461)
     if constexpr (OUT != kOutF32 && WN == 64) {
         static_assert(BM * BN * 2 <= 2 * kAB && (BM * BN * 2 <= kAB || W % 2 == 0), "in two stages");
@@ -356,10 +356,21 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
                 for (int k = 0; k < WM * LANES / 64; ++k) {
                     const uint32_t r = 64 / LANES * k + lane / LANES;
                     const int m = m0 + wm + int(r);
-                    if (m < a.M && n < a.N)
-                        store<decltype(past)::value>(reinterpret_cast<piece *>(d + int64_t(m) * a.ldd + n),
-                                                     *reinterpret_cast<const piece *>(mine + r * 128 + (((WIDE * c / 8) ^ (r & 7)) << 4) +
-                                                                                      2 * (WIDE * c % 8)));
+                    if (m >= a.M || n >= a.N)
+                        continue;
+                    const piece v = *reinterpret_cast<const piece *>(mine + r * 128 + (((WIDE * c / 8) ^ (r & 7)) << 4) +
+                                                                     2 * (WIDE * c % 8));
+                    T *const to = d + int64_t(m) * a.ldd + n;
+                    // (a pitch of whole pieces does not make N one: behind column N lies
+                    // what is not D's)
+                    if (WIDE != 4 || n + WIDE <= a.N) {
+                        store<decltype(past)::value>(reinterpret_cast<piece *>(to), v);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < WIDE; ++e)
+                            if (n + e < a.N)
+                                to[e] = v[e];
+                    }
                 }
             };
             if (vec == 2)
