@@ -101,7 +101,8 @@ enum {
  *           most 2^22
  * A NaN gives a NaN and takes no part in its block's largest; a block with an
  * infinity has an infinite scale, zeros where its values are finite and NaN
- * where they are not.  X has fewer than 2^23 blocks of 128 x 128.
+ * where they are not.  What is or becomes zero keeps its sign.  X has fewer than
+ * 2^23 blocks of 128 x 128.
  * Returns MSWZ_OK, MSWZ_ERR_INVALID or MSWZ_ERR_UNSUPPORTED.
  */
 int quant_fp8_plan_create(quant_fp8_plan **out, int64_t M, int64_t K, int dt, int block, int scales, int64_t ldx);

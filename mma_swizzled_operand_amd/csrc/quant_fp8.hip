@@ -55,7 +55,7 @@ __device__ __forceinline__ float scale_of(float most, bool pow2)
 }
 
 // What the values of a block are divided with: 1 / s in two parts, so that
-// x hi + x lo is within (1/2 + 2^-20) ulp of x / s and x / s itself where that is
+// x hi + x lo is within (1/2 + 2^-13) ulp of x / s and x / s itself where that is
 // a value of fp32.  The result need not be the quotient: it has to lie on the
 // quotient's side of every midpoint between two E4M3 values (five significant
 // bits at most), or on it.
@@ -67,12 +67,14 @@ __device__ __forceinline__ float scale_of(float most, bool pow2)
 // close to m, and then it lies above or below as s was rounded down or up: the
 // same way for all of a block, which the lower part of 1 / s takes in with a
 // step of 2^-20.  (s exact, or a power of two: no step, and the quotient comes
-// out exactly.)
+// out exactly.)  The upper part is 2^-19 of itself below 1 / s, so that the lower
+// one is above zero with either step: with parts of opposite signs -0 would
+// become 0.
 //
 // fp32 x.  te, the sum with its last bit cleared, is within 1.5 ulp of x / s, so
 // it lies on the same side of every midpoint or on it.  The sign of the exact
 // remainder x - te s then moves it one ulp towards x / s, off the midpoint and
-// not as far as the next one.
+// not as far as the next one; a zero gets its sign back at the end.
 template <int IN>
 struct Divisor {
     float hi, lo, s;   // (s: fp32 x only)
@@ -80,13 +82,18 @@ struct Divisor {
     __device__ Divisor() {}
     __device__ Divisor(float scale, float most, bool pow2) : s(scale)
     {
-        hi = 1.0f / s;
+        const float inverse = 1.0f / s;
         // an infinite scale: finite values give 0, infinite ones NaN
-        lo = hi == 0.0f ? 0.0f : fmaf(-s, hi, 1.0f) * hi;
+        hi = lo = 0.0f;
+        if (inverse == 0.0f)
+            return;
+        hi = IN == kOutF32 ? inverse : inverse * (1.0f - 0x1p-19f);
+        float rest = fmaf(-s, hi, 1.0f);
         if (IN != kOutF32 && !pow2) {
             const float over = fmaf(s, 448.0f, -most);   // (the sign is exact)
-            lo += over > 0.0f ? hi * -0x1p-20f : over < 0.0f ? hi * 0x1p-20f : 0.0f;
+            rest += over > 0.0f ? -0x1p-20f : over < 0.0f ? 0x1p-20f : 0.0f;
         }
+        lo = rest * inverse;
     }
     __device__ float operator()(float x) const
     {
@@ -96,7 +103,7 @@ struct Divisor {
         const float te = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, t) & ~1u);
         const float r = fmaf(-te, s, x);
         const float step = te * 0x1.8p-24f;
-        return te + __builtin_amdgcn_fmed3f(r * (hi * 0x1p25f), -step, step);
+        return copysignf(te + __builtin_amdgcn_fmed3f(r * (hi * 0x1p25f), -step, step), x);
     }
 };
 
