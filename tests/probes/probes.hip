@@ -9,10 +9,13 @@
 //     kernels use (E4M3 0, E2M3 2, E3M2 3, E2M1 4): operand bytes / values,
 //     scale lanes, the internal K index by which mixed formats meet;
 //   - the transposing LDS read ds_read_b64_tr_b16.
+// One more runs on the host alone: the kernel that a product of E4M3 operands
+// takes (fp8_choice.hpp).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "device_common.hpp"
+#include "fp8_choice.hpp"
 
 using namespace mswz;
 
@@ -141,6 +144,20 @@ int probe_read_tr16(const uint16_t *init, int n, const uint32_t *addrs, uint32_t
     k_read_tr16<<<1, 64>>>(static_cast<const uint16_t *>(di.p), n, static_cast<const uint32_t *>(dad.p),
                            static_cast<u32x2 *>(dout.p));
     return down(out, dout, 64 * 8);
+}
+
+// The number in Fp8Kernel's order; d_kind: 0 fp32, 1 bf16, 2 fp16.
+int probe_fp8_kernel(int M, int N, int K, int d_kind, int64_t lda, int64_t ldb)
+{
+    Fp8Args a{};
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.kb = (K + kFp8Block - 1) / kFp8Block;
+    a.lda = lda;
+    a.ldb = ldb;
+    a.out = d_kind == 0 ? kOutF32 : d_kind == 1 ? kOutBf16 : kOutF16;
+    return fp8_kernel(a);
 }
 
 }  // extern "C"

@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import mma_swizzled_operand_amd as mswz
+from test_gpu_fp8 import close, fp8_inputs, fp8_reference, fp8_run, gen
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +72,24 @@ def test_product_writes_its_columns_only(kernel, d, block, more):
         E.copy_((ref + old).to(DT[d]))
         mswz.gemm_run_fp8(plan, A, SA, B, SB, D, beta=1, workspace=ws)
         assert torch.equal(flat, want), (pitch, start, "beta")
+
+
+@pytest.mark.parametrize("block", ["row", "tile"])
+@pytest.mark.parametrize("kernel,d", CASES)
+def test_all_codes_by_every_kernel(kernel, d, block):
+    """Every finite code of both operands, subnormal ones and zeros among them: rows and columns at the edges of
+    tiles and in between, within the tolerance that test_gpu_fp8.py derives."""
+    M, N, K = shape_of(kernel, d)
+    N += 3
+    x = fp8_inputs(gen(M + N), M, N, K, block, subnormal=True)
+    x["SA"] *= 0.1      # (sums stay inside fp16)
+    plan = mswz.gemm_fp8_plan_create(M, N, K, d, block)
+    got = fp8_run(plan, x, torch.full((M, N), float("nan"), dtype=DT[d], device="cuda")).cpu()
+    assert torch.isfinite(got).all()
+    rows = torch.tensor(sorted({0, M // 2, M - 1, min(31, M - 1), min(64, M - 1)}))
+    ref, tol = fp8_reference(x["A"][rows], x["SA"][:, rows], x["B"], x["SB"], block == "tile", d == "f32")
+    close(got[rows], ref, tol, d, "rows")
+    cols = torch.tensor([0, 15, 63, 64, 127, 128, N // 2, N - 2, N - 1])
+    sb = x["SB"][cols // 128].t().contiguous() if block == "tile" else x["SB"][:, cols]
+    ref, tol = fp8_reference(x["A"], x["SA"], x["B"][cols], sb, False, d == "f32")
+    close(got[:, cols], ref, tol, d, "columns")
