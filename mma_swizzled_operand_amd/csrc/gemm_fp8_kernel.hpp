@@ -356,29 +356,28 @@ gemm_fp8_kernel(Fp8Args a, int tiles_m, int tiles_n, int group_m, int steps_per_
                 for (int k = 0; k < WM * LANES / 64; ++k) {
                     const uint32_t r = 64 / LANES * k + lane / LANES;
                     const int m = m0 + wm + int(r);
-                    if (m >= a.M || n >= a.N)
-                        continue;
-                    const piece v = *reinterpret_cast<const piece *>(mine + r * 128 + (((WIDE * c / 8) ^ (r & 7)) << 4) +
-                                                                     2 * (WIDE * c % 8));
-                    T *const to = d + int64_t(m) * a.ldd + n;
-                    // (a pitch of whole pieces does not make N one: behind column N lies
-                    // what is not D's)
-                    if (WIDE != 4 || n + WIDE <= a.N) {
-                        store<decltype(past)::value>(reinterpret_cast<piece *>(to), v);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < WIDE; ++e)
-                            if (n + e < a.N)
-                                to[e] = v[e];
-                    }
+                    if (m < a.M && n + WIDE <= a.N)
+                        store<decltype(past)::value>(reinterpret_cast<piece *>(d + int64_t(m) * a.ldd + n),
+                                                     *reinterpret_cast<const piece *>(mine + r * 128 + (((WIDE * c / 8) ^ (r & 7)) << 4) +
+                                                                                      2 * (WIDE * c % 8)));
                 }
             };
-            if (vec == 2)
+            if (vec == 2) {
                 rows(std::integral_constant<int, 8>{}, std::true_type{});
-            else if (vec == 1)
+            } else if (vec == 1) {
                 rows(std::integral_constant<int, 4>{}, std::false_type{});
-            else
+                // the up to three columns behind the last whole piece, a row a lane
+                // (5432 x 3691 x 1712 with a pitch of 3692 57.5 us, 3696 columns with one of
+                // 3700 57.5; as a branch in the loop above both 58.2)
+                const int n = a.N & ~3, c = n - n0 - wn;
+                if (n < a.N && c >= 0 && c < 64)
+                    for (int r = lane; r < WM && m0 + wm + r < a.M; r += 64)
+                        for (int e = 0; n + e < a.N; ++e)
+                            d[int64_t(m0 + wm + r) * a.ldd + n + e] =
+                                *reinterpret_cast<const T *>(mine + r * 128 + (((c / 8) ^ (r & 7)) << 4) + 2 * (c % 8 + e));
+            } else {
                 rows(std::integral_constant<int, 1>{}, std::false_type{});
+            }
             return;
         }
     }

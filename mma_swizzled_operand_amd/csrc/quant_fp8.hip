@@ -55,8 +55,9 @@ __device__ __forceinline__ float scale_of(float most, bool pow2)
 }
 
 // What the values of a block are divided with: 1 / s in two parts, so that
-// x hi + x lo is within (1/2 + 2^-13) ulp of x / s and x / s itself where that is
-// a value of fp32.  The result need not be the quotient: it has to lie on the
+// x hi + x lo is within (1/2 + 2^-6) ulp of x / s (the lower part is subnormal, with
+// an error of 2^-31 of the upper one, where s is near fp32's largest) and x / s
+// itself where that is a value of fp32.  The result need not be the quotient: it has to lie on the
 // quotient's side of every midpoint between two E4M3 values (five significant
 // bits at most), or on it.
 //
