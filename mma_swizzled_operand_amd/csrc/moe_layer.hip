@@ -639,6 +639,7 @@ struct Staged {
             o.acc[t][0] = o.acc[t][1] = f32x4{};
         Unit d[kUnits];
         copy(o, stage0, place(0), token_bytes, wave);
+        __builtin_amdgcn_sched_barrier(0);   // (the wait below counts the loads behind the copies)
         static_for<0, kUnits>([&](auto i) {
             load(o, d[i], place(0) * kUnits + i, whole, g, i % 2 == 1);
             __builtin_amdgcn_sched_barrier(0);
