@@ -49,6 +49,9 @@ typedef struct moe_layer_plan moe_layer_plan;
  * [ceil(I/128)][ceil(H/128)], the gate's tiles and the other half's, counted
  * from the first row of each; S2 [E][ceil(H/128)][ceil(I/128)].  With I a
  * multiple of 128, S1 is quant_fp8's tile scales of the whole W1.
+ * E4M3 weights have this call only: gemm_run_grouped takes 16-bit ones, so more
+ * choices than it allows are a gemm_run_fp8 for each expert and matrix, with the
+ * experts' row counts on the host.
  * Sums are fp32; between the two products a value keeps 16 significant bits
  * and fp32's range; Y is rounded once to nearest even.  A weight or value that
  * is not finite makes the outputs that it enters infinite or NaN.

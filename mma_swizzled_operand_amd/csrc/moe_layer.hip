@@ -14,11 +14,13 @@
 // choices an expert or more, both products take the tokens' values from LDS
 // (Staged).
 //
-// 16 tokens, 4 of 32 experts of 4096 x 2048 bf16: 215 us, kernels 143, 70 and 5, 5.8
-// TB/s of weights (a copy: 4.9).  64 tokens, 8 of 64 of 2048 x 1024 E4M3: 94 us,
-// kernels 56, 33 and 5, 4.5 TB/s while they run: their starts and ends are a
-// larger share.  One token, 2 of 8 of 1024 x 512: 12 us, two launches of three
-// dependent reads each.
+// 16 tokens, 4 of 32 experts of 4096 x 2048 bf16, by the experts in use: 16 of them
+// 150 us, 20 to 24 204 to 218, 25 to 32 263 to 286 (4.8 to 5.6 TB/s of weights; a
+// copy: 4.9): both products have 32 workgroups an expert, so 2, 3 or 4 for a compute
+// unit; of 215 the three kernels take 144, 70 and 5.  64 tokens, 8 of 64 of 2048 x
+// 1024 E4M3: 91 to 95 us with 59 to 61 in use, kernels 56, 33 and 5, 4.4 TB/s while
+// the products run: their starts and ends are a larger share.  One token, 2 of 8 of
+// 1024 x 512: 12 us, two launches of three dependent reads each.
 //
 // 16x16x32 MFMAs, the weights first: lane l holds 8 values of weight row
 // l % 16 (of token l % 16 as the second operand), and its four results are
